@@ -3,10 +3,10 @@
 // device memory or waits for the device, except moe_read_device_status and the host
 // pipeline's create (streams and events) and destroy (waits for its copies).
 #include <atomic>
-#include <initializer_list>
 #include <mutex>
 #include <string.h>
 
+#include "checks.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
 #include "launch.cuh"
@@ -142,37 +142,6 @@ Layout layout_of(const moe_shape_t& s) {
   if (s.combine == MOE_COMBINE_FUSED) o = align_up(o + T * H * 4);
   L.total = o;
   return L;
-}
-
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// all given pointers non-null and 16-byte aligned
-int check_ptrs(std::initializer_list<const void*> ps) {
-  for (const void* p : ps) {
-    if (!p) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
-  }
-  return MOE_OK;
-}
-// optional pointers: may be null, else aligned
-int check_opt(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (p && !aligned16(p)) return MOE_ERR_ALIGNMENT;
-  return MOE_OK;
-}
-
-inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
-inline int cuda_rc(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
-#define MOE_TRY(expr)            \
-  do {                           \
-    const int _rc = (expr);      \
-    if (_rc != MOE_OK) return _rc; \
-  } while (0)
-
-template <typename T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
 }
 
 int route_impl(const moe_shape_t* s, const void* x, const float* w_router, const void* w_packed,

@@ -34,6 +34,11 @@ struct DeviceInfo {
 // Cached per device; returns MOE_OK, MOE_ERR_CUDA or MOE_ERR_NO_DEVICE.
 int current_device_info(DeviceInfo* info);
 
+// Tensor map of a row-major byte matrix: boxes of 128 bytes x box_rows rows, 128-byte swizzle,
+// zeros past the last row and past the row's end.
+int make_byte_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_bytes,
+                  uint32_t box_rows);
+
 // Two int32 buffers that a kernel clears (after its dependency wait) for the kernels
 // after it: the router kernels clear the expert counts and the FFN-pick histogram that
 // the top-K kernel then accumulates into.

@@ -1,0 +1,130 @@
+// mx4.cuh - the microscaled 4-bit formats on the device and the host: block scales, e2m1
+// rounding, the scale layout, and the description of a 4-bit matrix that the kernels take.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "../../include/moe_mx4.h"
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kMx4MaxGroups = 1024;
+
+// elements that share a scale
+__host__ __device__ constexpr int mx4_block(bool nv) { return nv ? 16 : 32; }
+
+// A 4-bit matrix as the kernels see it (moe_mx4_t without the buffers).
+struct Mx4Rows {
+  const int32_t* offsets;   // ragged groups, or null
+  int rows, K, groups, group_rows;
+
+  __device__ __forceinline__ int begin(int g) const { return offsets ? offsets[g] : g * group_rows; }
+};
+
+// Byte offset of the scale of block b in row l of the group that starts at row o_g: pieces of
+// 128 rows x 4 blocks, 512 bytes each, as tcgen05.cp hands them to the tensor cores (32 lanes
+// of 16 bytes: lane l % 32 holds the four scales of its rows l % 32 + 0, 32, 64, 96).
+// `chunks` is the number of pieces along K.
+__device__ __forceinline__ size_t mx4_scale_at(int o_g, int g, int l, int b, int chunks) {
+  const size_t tile = (size_t)(o_g >> 7) + g + (l >> 7);
+  return (tile * chunks + (b >> 2)) * 512 + (l & 31) * 16 + ((l & 127) >> 5) * 4 + (b & 3);
+}
+
+// Group of row r, for a whole warp with one r: the groups' starts are searched 32 at a time.
+// -1 when no group has the row. Returns the group's first row in o_g.
+__device__ __forceinline__ int mx4_find_group(const Mx4Rows& m, int r, int& o_g) {
+  if (r >= m.rows) return -1;
+  if (!m.offsets) {
+    const int g = r / m.group_rows;
+    o_g = g * m.group_rows;
+    return g;
+  }
+  // the last start that is <= r; empty groups share their start with the next one
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = m.groups + 1;         // starts [lo, lo + n) are candidates
+  while (n > 32) {
+    const int step = (n + 31) / 32;
+    const int at = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, lane * step < n && m.offsets[at] <= r);
+    if (!le) return -1;
+    const int k = 31 - __clz(le);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  const unsigned le = __ballot_sync(0xffffffffu, lane < n && m.offsets[lo + min(lane, n - 1)] <= r);
+  if (!le) return -1;
+  const int g = lo + 31 - __clz(le);
+  if (g >= m.groups) return -1;
+  o_g = m.offsets[g];
+  return g;
+}
+
+// Two floats -> two e2m1 numbers in a byte (a in the low half), nearest even, at most 6.
+__device__ __forceinline__ uint32_t e2m1x2(float a, float b) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 q;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q, %2, %1;\n\t"
+      "cvt.u32.u8 %0, q;\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b));
+  return r;
+}
+
+// Nearest e4m3 number of a non-negative float, at most 448; NaN for a NaN.
+__device__ __forceinline__ uint32_t e4m3(float a) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(a));
+  return r & 0xFFu;
+}
+__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)byte));
+  __half_raw v;
+  v.x = (unsigned short)(h & 0xFFFFu);
+  return __half2float(__half(v));
+}
+// 2^(byte - 127); 255 is NaN
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7FC00000u : byte ? byte << 23 : 1u << 22);
+}
+
+// A block's scale byte, and what its elements are divided (NVFP4) or multiplied (MXFP4) by
+// before rounding, from the bits of the block's largest magnitude (as unsigned integers the
+// magnitudes of floats are in order, and those of infinity and NaN are the largest). `by` is 0
+// where every element rounds to 0: an empty block, or one without a finite scale.
+template <bool NV>
+__device__ __forceinline__ uint32_t mx4_scale(uint32_t amax_bits, float t, float& by) {
+  by = 0.f;
+  if (NV) {
+    if (amax_bits >= 0x7F800000u) return 0x7Fu;
+    const uint32_t s = e4m3(__fdiv_rn(__uint_as_float(amax_bits), __fmul_rn(6.0f, t)));
+    if (s != 0u) by = __fmul_rn(e4m3_value(s), t);
+    return s;
+  }
+  const uint32_t e = amax_bits >> 23;
+  if (e == 255u) return 255u;
+  const uint32_t b = e > 2u ? e - 2u : 0u;
+  by = __uint_as_float((254u - b) << 23);
+  return b;
+}
+// An element on the grid of its block, before rounding.
+template <bool NV>
+__device__ __forceinline__ float mx4_scaled(float x, float by) {
+  if (NV) return by != 0.f ? __fdiv_rn(x, by) : 0.f;
+  return by != 0.f ? __fmul_rn(x, by) : 0.f;     // (inf or NaN) * 0 would not be 0
+}
+
+// ---- host side -------------------------------------------------------------------------------
+// Checks a matrix's sizes (MOE_OK or an error).
+int mx4_check(const moe_mx4_t* m);
+inline bool is_nv(const moe_mx4_t& m) { return m.format == MOE_MX4_NVFP4; }
+inline size_t mx4_scale_tiles(const moe_mx4_t& m) { return (size_t)(m.rows / 128) + m.groups; }
+inline size_t mx4_scale_size(const moe_mx4_t& m) {
+  return mx4_scale_tiles(m) * (m.K / (4 * mx4_block(is_nv(m)))) * 512;
+}
+inline Mx4Rows mx4_rows(const moe_mx4_t& m) {
+  return Mx4Rows{m.offsets, m.rows, m.K, m.groups, m.group_rows};
+}
+
+}  // namespace moe

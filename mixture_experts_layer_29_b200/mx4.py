@@ -1,0 +1,295 @@
+"""The layer's experts in microscaled 4-bit floating point (include/moe_mx4.h).
+
+Two formats: "mxfp4" (blocks of 32 with a power-of-two scale) and "nvfp4" (blocks of 16 with an
+e4m3 scale times one fp32 factor per matrix or group). A `Matrix` is a 4-bit matrix on the
+device: packed codes, block scales in the tensor cores' layout, and the rows' groups.
+
+    a = mx4.allocate("mxfp4", rows, H, groups=n, offsets=offsets)   # ragged rows
+    w = mx4.quantize_weight(w_bf16, "mxfp4")                        # [n, N, H], once
+    mx4.quantize(x, a)
+    mx4.grouped_gemm(a, w, out, mx4.gemm_workspace())               # out[r] = a[r] . w[g]^T
+
+The calls marshal arguments only, like `abi`: the arithmetic runs in the library's kernels,
+there is no fallback, and an error code raises abi.MoEError. Tensors are checked here for type,
+device and contiguity (ValueError). Inference only: the 4-bit product has no backward.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+import re
+
+import torch
+
+from . import abi
+
+HEADER = os.path.join(os.path.dirname(abi.HEADER), "moe_mx4.h")
+FORMATS = {"mxfp4": 0, "nvfp4": 1}
+BLOCK = {"mxfp4": 32, "nvfp4": 16}
+_DTYPES = {torch.bfloat16: abi.MOE_BF16, torch.float32: abi.MOE_FP32}
+
+
+class Desc(ctypes.Structure):
+    """moe_mx4_t"""
+    _fields_ = [("format", ctypes.c_int32), ("rows", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("group_rows", ctypes.c_int32),
+                ("factor_per_group", ctypes.c_int32), ("offsets", ctypes.c_void_p),
+                ("factor", ctypes.c_void_p), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
+
+
+_P, _SZ, _I32, _I64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
+_D = ctypes.POINTER(Desc)
+_SIGS = {
+    "moe_mx4_scale_bytes": [_D, ctypes.POINTER(_SZ)],
+    "moe_mx4_quantize": [_D, _P, _I32, _I64, _P, _I32, _I32, _P, _P],
+    "moe_mx4_dequantize": [_D, _P, _I32, _I64, _P],
+    "moe_mx4_pack_scales": [_D, _P, _P],
+    "moe_mx4_gemm_workspace_size": [ctypes.POINTER(_SZ)],
+    "moe_mx4_grouped_gemm": [_D, _D, _P, _I32, _P, _SZ, _P],
+    "moe_mx4_ffn_workspace_size": [_D, _D, ctypes.POINTER(_SZ)],
+    "moe_mx4_grouped_ffn": [_D, _D, _D, _P, _P, _P, ctypes.c_float, _P, _I32, _P, _SZ, _P],
+}
+_lib = None
+
+
+def lib() -> ctypes.CDLL:
+    """The library (abi.lib()) with this header's signatures set."""
+    global _lib
+    if _lib is None:
+        L = abi.lib()
+        for name, args in _SIGS.items():
+            f = getattr(L, name)
+            f.restype, f.argtypes = ctypes.c_int, args
+        _lib = L
+    return _lib
+
+
+def header_functions() -> list[str]:
+    """Names of the functions include/moe_mx4.h declares."""
+    return sorted(set(re.findall(r"^int\s+(moe_\w+)\s*\(", open(HEADER).read(), flags=re.M)))
+
+
+def _call(name: str, *args):
+    abi._check(getattr(lib(), name)(*args), name)
+
+
+def _tensor(t, name, dtypes, shape=None, device=None, optional=False, contiguous=True):
+    """Checks one tensor argument and returns its address (None for an absent optional one)."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+class Matrix:
+    """A 4-bit matrix: rows of K elements in groups (see include/moe_mx4.h for the layout).
+
+    codes [rows, K / 2] uint8, scales uint8, offsets int32 [groups + 1] (ragged groups) or None
+    (groups of rows / groups rows each), tensor_scale fp32 [1] or [groups] (nvfp4) or None."""
+
+    def __init__(self, fmt, rows, K, groups=1, offsets=None, tensor_scale=None, codes=None,
+                 scales=None, device="cuda"):
+        if fmt not in FORMATS:
+            raise ValueError(f"format {fmt!r}: one of {sorted(FORMATS)}")
+        if offsets is None and groups > 0 and rows % groups != 0:
+            raise ValueError(f"{rows} rows in {groups} equal groups: give offsets")
+        if tensor_scale is not None and tensor_scale.numel() not in (1, groups):
+            raise ValueError(f"tensor_scale: {tensor_scale.numel()} values, expected 1 or {groups}")
+        self.fmt, self.rows, self.K, self.groups = fmt, rows, K, groups
+        self.offsets, self.tensor_scale = offsets, tensor_scale
+        d = self._sizes()
+        n = _SZ(0)
+        _call("moe_mx4_scale_bytes", ctypes.byref(d), ctypes.byref(n))
+        self.codes = torch.empty(rows, K // 2, dtype=torch.uint8, device=device) if codes is None else codes
+        self.scales = torch.empty(n.value, dtype=torch.uint8, device=device) if scales is None else scales
+        if self.scales.numel() < n.value:
+            raise ValueError(f"scales: {self.scales.numel()} bytes, expected {n.value}")
+
+    def _sizes(self) -> Desc:
+        ts = self.tensor_scale
+        return Desc(FORMATS[self.fmt], self.rows, self.K, self.groups,
+                    0 if self.offsets is not None else self.rows // max(self.groups, 1),
+                    int(ts is not None and ts.numel() > 1), None, None, None, None)
+
+    def desc(self) -> Desc:
+        """The matrix as the C ABI takes it; checks the buffers."""
+        d = self._sizes()
+        d.offsets = _tensor(self.offsets, "offsets", (torch.int32,), (self.groups + 1,), optional=True)
+        d.factor = _tensor(self.tensor_scale, "tensor_scale", (torch.float32,), optional=True)
+        d.codes = _tensor(self.codes, "codes", (torch.uint8,))
+        if self.codes.numel() != self.rows * (self.K // 2):
+            raise ValueError(f"codes: {self.codes.numel()} bytes, expected {self.rows * (self.K // 2)}")
+        d.scales = _tensor(self.scales, "scales", (torch.uint8,))
+        return d
+
+
+def allocate(fmt, rows, K, groups=1, offsets=None, tensor_scale=None, device="cuda") -> Matrix:
+    """A Matrix with room for `rows` rows; quantize() fills it. offsets: device int32
+    [groups + 1], read by every call (they may change between calls)."""
+    return Matrix(fmt, rows, K, groups, offsets, tensor_scale, device=device)
+
+
+def from_checkpoint(fmt, codes, scales, tensor_scale=None, stream=None) -> Matrix:
+    """A weight from a 4-bit checkpoint: codes [groups, N, K / 2] uint8 (used as they are) and
+    row-major block scales [groups, N, K / B] uint8, laid out for the tensor cores here, once."""
+    groups, N, half = codes.shape
+    m = Matrix(fmt, groups * N, 2 * half, groups, None, tensor_scale, codes=codes, device=codes.device)
+    p = _tensor(scales, "scales", (torch.uint8,), (groups, N, m.K // BLOCK[fmt]))
+    _call("moe_mx4_pack_scales", ctypes.byref(m.desc()), p, abi._stream(stream))
+    return m
+
+
+def quantize_weight(w, fmt, tensor_scale=None, stream=None) -> Matrix:
+    """A weight [groups, N, K] bf16 or fp32 in 4 bits, once, at load time."""
+    groups, N, K = w.shape
+    m = Matrix(fmt, groups * N, K, groups, None, tensor_scale, device=w.device)
+    return quantize(w.reshape(groups * N, K), m, stream=stream)
+
+
+def _rows(t, name, m, rows):
+    """(address, dtype code, row stride) of a [rows, K] operand whose rows may be strided."""
+    p = _tensor(t, name, tuple(_DTYPES), (rows, m.K), contiguous=False)
+    if rows and m.K > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: elements of a row are not adjacent")
+    ld = t.stride(0) if rows > 1 else m.K
+    return p, _DTYPES[t.dtype], ld
+
+
+def quantize(x, m: Matrix, row_of=None, status=None, stream=None) -> Matrix:
+    """Rounds x into m. Without row_of, row r of m is row r of x [rows, K]. With row_of int32
+    [tokens, picks] (abi.permute's), row t of x [tokens, K] goes to each row row_of[t, p] >= 0
+    of m. status: a device int32 that receives a device-side check's failure (a workspace's
+    first word, for abi.read_device_status)."""
+    tokens, picks = m.rows, 0
+    if row_of is not None:
+        if row_of.dim() != 2:
+            raise ValueError("row_of: [tokens, picks]")
+        tokens, picks = row_of.shape
+    p, dt, ld = _rows(x, "x", m, tokens)
+    _call("moe_mx4_quantize", ctypes.byref(m.desc()), p, dt, ld,
+          _tensor(row_of, "row_of", (torch.int32,), optional=True), tokens, picks,
+          None if status is None else status.data_ptr(), abi._stream(stream))
+    return m
+
+
+def dequantize(m: Matrix, out, stream=None):
+    """The values of m into out [rows, K] bf16 or fp32 (rows of no group are left alone)."""
+    p, dt, ld = _rows(out, "out", m, m.rows)
+    _call("moe_mx4_dequantize", ctypes.byref(m.desc()), p, dt, ld, abi._stream(stream))
+    return out
+
+
+def gemm_workspace(device="cuda"):
+    n = _SZ(0)
+    _call("moe_mx4_gemm_workspace_size", ctypes.byref(n))
+    return torch.zeros(n.value, dtype=torch.uint8, device=device)
+
+
+def grouped_gemm(a: Matrix, w: Matrix, out, ws, stream=None):
+    """out[r] = a[r] . w[g]^T for the rows r of each group g; out [a.rows, N] bf16 or fp32."""
+    p = _tensor(out, "out", tuple(_DTYPES), (a.rows, w.rows // max(w.groups, 1)))
+    _call("moe_mx4_grouped_gemm", ctypes.byref(a.desc()), ctypes.byref(w.desc()), p,
+          _DTYPES[out.dtype], _tensor(ws, "ws", (torch.uint8,)), ws.numel(), abi._stream(stream))
+    return out
+
+
+def ffn_workspace(a: Matrix, w_gate_up: Matrix, device="cuda"):
+    """Workspace of grouped_ffn (status word and h), zeroed."""
+    n = _SZ(0)
+    _call("moe_mx4_ffn_workspace_size", ctypes.byref(a.desc()), ctypes.byref(w_gate_up.desc()),
+          ctypes.byref(n))
+    return torch.zeros(n.value, dtype=torch.uint8, device=device)
+
+
+def grouped_ffn(a: Matrix, w_gate_up: Matrix, w_down: Matrix, out, ws, h_scale=None, perm_token=None,
+                row_gate=None, scale=1.0, stream=None):
+    """The grouped SwiGLU FFN on 4-bit experts. Without perm_token: out [a.rows, H] bf16 or
+    fp32, one row each. With it (fused combine): out fp32 [tokens, H], to which
+    scale * row_gate[r] * y[r] is added at perm_token[r]."""
+    shape = (a.rows, a.K) if perm_token is None else (out.shape[0], a.K)
+    p = _tensor(out, "out", tuple(_DTYPES), shape)
+    one = (torch.float32,)
+    _call("moe_mx4_grouped_ffn", ctypes.byref(a.desc()), ctypes.byref(w_gate_up.desc()),
+          ctypes.byref(w_down.desc()), _tensor(h_scale, "h_scale", one, (1,), optional=True),
+          _tensor(perm_token, "perm_token", (torch.int32,), optional=True),
+          _tensor(row_gate, "row_gate", one, optional=True), float(scale), p, _DTYPES[out.dtype],
+          _tensor(ws, "ws", (torch.uint8,)), ws.numel(), abi._stream(stream))
+    return out
+
+
+class Mx4MoELayer:
+    """One LongCat-Flash MoE layer whose FFN experts are 4-bit: the router, the permutation, the
+    combine and the PID bias of abi.MoELayer around mx4.grouped_ffn. Each token's activations
+    are rounded once and written to its picks' rows.
+
+    w_gate_up, w_down: Matrix (quantize_weight or from_checkpoint). x_scale, h_scale: the
+    activations' nvfp4 factors, fp32 [1], or None. forward(x) returns what
+    abi.MoELayer.forward returns."""
+
+    def __init__(self, shape: abi.Shape, w_router, bias, w_gate_up: Matrix, w_down: Matrix,
+                 pid: abi.Pid | None = None, x_scale=None, h_scale=None):
+        if shape.dtype != abi.MOE_BF16:
+            raise ValueError("4-bit experts need a bf16 layer")
+        N = shape.n_ffn
+        for name, m, want in (("w_gate_up", w_gate_up, (N, N * 2 * shape.I, shape.H)),
+                              ("w_down", w_down, (N, N * shape.H, shape.I))):
+            if (m.groups, m.rows, m.K) != want or m.offsets is not None:
+                raise ValueError(f"{name}: {m.groups} groups of {m.rows} x {m.K} in all, expected {want}")
+        self.shape, self.w_router, self.bias = shape, w_router, bias
+        self.w_gate_up, self.w_down, self.h_scale, self.pid = w_gate_up, w_down, h_scale, pid
+        dev = w_gate_up.codes.device
+        T, H, K, rows = shape.T, shape.H, shape.K, shape.T * shape.K
+        i32, f32 = torch.int32, torch.float32
+        fused = shape.combine == abi.MOE_COMBINE_FUSED
+        self.scratch = torch.zeros(max(abi.scratch_size(shape), 256), dtype=torch.uint8, device=dev)
+        self.logits = torch.empty(T, shape.E, dtype=f32, device=dev)
+        self.topk_idx = torch.empty(T, K, dtype=i32, device=dev)
+        self.topk_gate = torch.empty(T, K, dtype=f32, device=dev)
+        self.counts = torch.empty(shape.E, dtype=i32, device=dev)
+        self.nffn_hist = torch.empty(K + 1, dtype=i32, device=dev)
+        self.zgate = torch.empty(T, dtype=f32, device=dev)
+        self.offsets = torch.zeros(N + 1, dtype=i32, device=dev)
+        self.perm_token = torch.empty(rows, dtype=i32, device=dev)
+        self.row_of = torch.empty(T, K, dtype=i32, device=dev)
+        self.row_gate = torch.empty(rows, dtype=f32, device=dev)
+        self.out_acc = torch.empty(T, H, dtype=f32, device=dev) if fused else None
+        self.y = None if fused else torch.empty(rows, H, dtype=torch.bfloat16, device=dev)
+        self.out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        self.a = allocate(w_gate_up.fmt, rows, H, N, self.offsets, x_scale, device=dev)
+        self.ws = ffn_workspace(self.a, w_gate_up, device=dev)
+        self.pid_state = torch.empty(3 * N, dtype=f32, device=dev)
+        self.stats = torch.zeros(8, dtype=f32, device=dev)
+        abi.pid_init(shape, bias, self.pid_state)
+
+    def forward(self, x, logits_in=None, stream=None):
+        s = self.shape
+        abi.route(s, x, self.w_router, logits_in, self.bias, None if logits_in is not None else self.logits,
+                  self.topk_idx, self.topk_gate, self.counts, self.nffn_hist, self.zgate, self.scratch, stream)
+        abi.permute(s, self.topk_idx, self.topk_gate, self.zgate, x, self.offsets, self.perm_token,
+                    self.row_of, self.row_gate, None, self.out_acc, self.scratch, stream)
+        quantize(x, self.a, self.row_of, self.ws, stream)
+        if self.out_acc is not None:
+            grouped_ffn(self.a, self.w_gate_up, self.w_down, self.out_acc, self.ws, self.h_scale,
+                        self.perm_token, self.row_gate, s.ffn_out_scale, stream)
+        else:
+            grouped_ffn(self.a, self.w_gate_up, self.w_down, self.y, self.ws, self.h_scale, stream=stream)
+        abi.combine(s, x, self.y, self.out_acc, self.topk_gate, self.row_of, self.zgate, self.out, stream)
+        return self.out, self.topk_idx, self.topk_gate, self.counts, self.nffn_hist
+
+    def update_bias(self, stream=None):
+        if self.pid is None:
+            raise ValueError("no PID gains given")
+        abi.pid_bias_update(self.pid, self.shape, self.counts, self.nffn_hist, self.bias, self.pid_state,
+                            self.stats, stream)
+        return self.stats
