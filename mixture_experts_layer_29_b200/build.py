@@ -22,7 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_b200.so")
 SOURCES = ["abi.cu", "router.cu", "permute.cu", "gemm_tc.cu", "ffn_simt.cu", "combine_pid.cu",
            "permute_static.cu", "lbloss.cu", "gemm_bwd.cu", "backward.cu", "mx4_quant.cu",
-           "mx4_gemm.cu"]
+           "mx4_gemm.cu", "block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]
