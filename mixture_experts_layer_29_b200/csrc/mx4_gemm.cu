@@ -14,11 +14,17 @@
 //   warp 0      TMA producer: per stage of K = 256 elements (128 bytes, 128-byte swizzle) two
 //               weight boxes of 128 rows, the tile's rows in boxes of 64 and 16, and the block
 //               scales as plain bulk copies of the 512-byte pieces
-//   warp 1      TMEM owner and MMA issuer: tcgen05.cp moves each piece of scales to its 4 TMEM
-//               columns, then 4 x 2 tcgen05.mma M128 K64 per stage
+//   warp 1      TMEM owner and MMA issuer: 4 x 2 tcgen05.mma M128 K64 per stage
 //   warps 2-9   epilogue: tcgen05.ld, math, global stores
-// The scales of a stage alternate between two TMEM slots: before it overwrites a slot the issuer
-// waits until the MMAs of two stages ago have completed.
+//   warps 10-13 scales: each warp copies the stage's pieces from shared memory to its lane quarter
+//               of TMEM with tcgen05.st (the MMA reads them in all four quarters)
+// The scales of a stage alternate between two TMEM slots: before the scale warps overwrite a slot
+// they wait until the MMAs of two stages ago have completed. tcgen05.cp would copy them without
+// these warps, but each copy of 512 bytes holds up the tensor pipe for some 90 cycles (8 to 16
+// copies per stage of 768): 64 experts' gate/up at a decode batch took 214 us with it.
+// A lane of the epilogue reads one channel of 8 rows; an 8 x 8 transposition over 8 lanes gives it 8
+// channels of one row, so that it rounds h with one block scale and stores 16 or 32 bytes at once
+// (one channel per lane took 190 us of 750 at 32768 rows, in 2-byte stores).
 //
 // Tiles: a group of `count` rows has ceil(count / NT) tiles along its rows; the table is built in
 // shared memory from `offsets` by every CTA, so the host never reads the counts. Columns past
@@ -39,11 +45,13 @@ namespace moe {
 namespace {
 
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + kEpiWarps * 32;
+constexpr int kScaleWarps = 4;
+constexpr int kThreads = 64 + (kEpiWarps + kScaleWarps) * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr int W_BYTES = 128 * 128;                  // a weight block's stage: 128 rows x 128 bytes
 
-enum Mode : int { kStore = 0, kAtomic = 1, kSwiglu = 2 };
+// kStore: y in bf16; kFp32: y in fp32, stored or added to the tokens' sums; kSwiglu: h in 4 bits
+enum Mode : int { kStore = 0, kFp32 = 1, kSwiglu = 2 };
 
 struct Args {
   Mx4Rows a;              // the rows' groups
@@ -59,11 +67,10 @@ struct Args {
   const float* w_factor;
   int w_factor_per_group;
   int mode;
-  void* out;              // kStore: [rows, n_out]; kAtomic: fp32 [*, n_out]; kSwiglu: h's codes
-  int out_fp32;
+  void* out;              // kStore, kFp32: [rows, n_out] (or tokens); kSwiglu: h's codes
   uint8_t* h_scales;      // kSwiglu
   const float* h_factor;
-  const int32_t* perm_token;   // kAtomic
+  const int32_t* perm_token;   // kFp32: row r is added to out[perm_token[r]]; or null
   const float* row_gate;
   float scale;
   int* status;
@@ -92,6 +99,7 @@ struct alignas(1024) Storage {
   uint64_t empty[STAGES];
   uint64_t tfull[2];
   uint64_t tempty[2];
+  uint64_t sfull[2];        // a slot of scales is in TMEM
   uint32_t tmem_base;
   int abort_flag;
   int offs[kMx4MaxGroups + 1];
@@ -129,13 +137,21 @@ __device__ __forceinline__ Tile decode(const S& s, const Args& g, int tile, int 
 }
 
 // ---- tcgen05 with block scales ---------------------------------------------------------------
-// 32 rows of 16 bytes in shared memory -> 4 TMEM columns of lanes 0-31, repeated in the other
-// three lane quarters.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t smem_addr) {
-  // no swizzle: 8-row groups of 16-byte rows, 128 bytes apart
-  const uint64_t desc = static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) |
-                        (static_cast<uint64_t>(128u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// P pieces of scales (512 bytes each, one after another) -> 4 P TMEM columns from taddr on, this
+// warp's lane quarter: lane l holds bytes [16 l, 16 l + 16) of each piece. `step` is the distance
+// of the pieces' columns.
+template <int P>
+__device__ __forceinline__ void tmem_st_scales(uint32_t taddr, int step, const uint8_t* pieces, int lane) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const uint4 v = *reinterpret_cast<const uint4*>(pieces + p * 512 + lane * 16);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr + p * step),
+                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // D (+)= (A * scales of A) (B * scales of B)^T, both operands e2m1, fp32 accumulate.
@@ -179,90 +195,98 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, float (&r)[8]) {
-  uint32_t u[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
-               : "r"(taddr));
+// 8 x 8 transposition over the lanes of each 8-lane group: lane i's v[j] goes to lane j's v[i].
+__device__ __forceinline__ void transpose8(float (&v)[8], int lane) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(u[i]);
+  for (int s = 4; s > 0; s >>= 1) {
+    const bool upper = lane & s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i & s) continue;
+      const float keep = upper ? v[i + s] : v[i];
+      const float got = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + s], s);
+      v[i] = upper ? got : keep;
+      v[i + s] = upper ? keep : got;
+    }
+  }
 }
 
-// Lane i of each 8-lane group holds 8 four-bit values, value j for column j; afterwards lane j
-// holds column j's values, value i from lane i.
-__device__ __forceinline__ uint32_t transpose_nibbles(uint32_t v, int lane) {
-  uint32_t o = __shfl_xor_sync(0xffffffffu, v, 4);
-  v = lane & 4 ? (v & 0xFFFF0000u) | (o >> 16) : (v & 0xFFFFu) | (o << 16);
-  o = __shfl_xor_sync(0xffffffffu, v, 2);
-  v = lane & 2 ? (v & 0xFF00FF00u) | ((o >> 8) & 0x00FF00FFu) : (v & 0x00FF00FFu) | ((o & 0x00FF00FFu) << 8);
-  o = __shfl_xor_sync(0xffffffffu, v, 1);
-  v = lane & 1 ? (v & 0xF0F0F0F0u) | ((o >> 4) & 0x0F0F0F0Fu) : (v & 0x0F0F0F0Fu) | ((o & 0x0F0F0F0Fu) << 4);
-  return v;
-}
-
-// ---- epilogues: 8 columns (rows of the tile) at a time, lane = channel -------------------------
-// h: 32 channels of a warp are one (MXFP4) or two (NVFP4) blocks of each of the 8 rows.
+// ---- epilogues: 8 rows of the tile from row c on; v: 8 channels, from channel ch on, of row
+// c + lane % 8 ------------------------------------------------------------------------------
+// h rounded to 4 bits: the warp's 32 channels are one (MXFP4) or two (NVFP4) blocks of each row.
+// hf: h's factor, inv6 = 1 / (6 hf). h comes out of an fp32 accumulation, so NVFP4 divides by way
+// of reciprocals here: that moves h by two units in its last place at most.
 template <bool NV>
-__device__ __forceinline__ void epi_swiglu(const Args& a, const Tile& t, int c, int q, int lane, float f,
-                                           float (&gate)[8], float (&up)[8], float hf) {
-  uint32_t byte[8], v = 0;
+__device__ __forceinline__ void epi_round_h(const Args& a, const Tile& t, int c, int ch, int lane,
+                                            const float (&h)[8], float hf, float inv6) {
+  uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    float s[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float G = gate[j + i] * f, U = up[j + i] * f;
-      const float h = __fdividef(G, 1.0f + __expf(-G)) * U;
-      const uint32_t bits = __float_as_uint(h) & 0x7FFFFFFFu;
-      uint32_t top;
-      if (NV) {
-        const uint32_t lo = __reduce_max_sync(0xffffffffu, lane < 16 ? bits : 0u);
-        const uint32_t hi = __reduce_max_sync(0xffffffffu, lane < 16 ? 0u : bits);
-        top = lane < 16 ? lo : hi;
-      } else {
-        top = __reduce_max_sync(0xffffffffu, bits);
-      }
-      float by;
-      byte[j + i] = mx4_scale<NV>(top, hf, by);
-      s[i] = mx4_scaled<NV>(h, by);
-    }
-    v |= e2m1x2(s[0], s[1]) << (4 * j);
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+  if (!NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+  float by = 0.f;
+  uint32_t byte;
+  if (NV) {
+    byte = top >= 0x7F800000u ? 0x7Fu : e4m3(__uint_as_float(top) * inv6);
+    if (top < 0x7F800000u && byte != 0u) by = 1.0f / (e4m3_value(byte) * hf);
+  } else {
+    byte = mx4_scale<false>(top, 1.0f, by);
   }
-  v = transpose_nibbles(v, lane);
-  const int j = lane & 7, quad = lane >> 3;
-  const int row = t.row0 + c + j;
-  // this lane's block's scale of row j
-  uint32_t b = byte[0];
+  uint32_t v = 0;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) b = j == i ? byte[i] : b;
+  for (int i = 0; i < 8; i += 2)
+    v |= e2m1x2(by != 0.f ? h[i] * by : 0.f, by != 0.f ? h[i + 1] * by : 0.f) << (4 * i);
+  const int j = lane & 7;
   if (c + j >= t.n) return;
-  const int ch = t.n0 + 32 * q;
-  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + (size_t)row * (a.n_out / 2) + ch / 2 + 4 * quad) = v;
-  if (quad == 0 || (NV && quad == 2)) {
-    const int block = (ch + 8 * quad) / mx4_block(NV);
-    a.h_scales[mx4_scale_at(t.o_g, t.g, row - t.o_g, block, a.n_out / (4 * mx4_block(NV)))] = (uint8_t)b;
-  }
+  const int row = t.row0 + c + j;
+  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + (size_t)row * (a.n_out / 2) + ch / 2) = v;
+  if (lane < 8 || (NV && (lane & 8) == 0))
+    a.h_scales[mx4_scale_at(t.o_g, t.g, row - t.o_g, ch / mx4_block(NV), a.n_out / (4 * mx4_block(NV)))] =
+        (uint8_t)byte;
 }
 
-__device__ __forceinline__ void epi_plain(const Args& a, const Tile& t, int c, int ch, float f,
-                                          const float (&y)[8]) {
-  if (ch >= a.n_out) return;
+// y, times f: 16 (bf16) or 32 bytes per lane, 64 or 128 contiguous bytes per row and warp, where
+// rows are 16-byte aligned; else value by value.
+template <int MODE>
+__device__ __forceinline__ void epi_store(const Args& a, const Tile& t, int c, int ch, int lane, float f,
+                                          float (&v)[8]) {
+  if (c + (lane & 7) >= t.n || ch >= a.n_out) return;
+  const int row = t.row0 + c + (lane & 7);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (c + j >= t.n) break;
-    const int row = t.row0 + c + j;
-    if (a.mode == kAtomic) {
-      atomicAdd(static_cast<float*>(a.out) + (size_t)a.perm_token[row] * a.n_out + ch,
-                a.scale * a.row_gate[row] * f * y[j]);
-    } else if (a.out_fp32) {
-      static_cast<float*>(a.out)[(size_t)row * a.n_out + ch] = f * y[j];
+  for (int i = 0; i < 8; ++i) v[i] *= f;
+  if (MODE == kStore) {
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (size_t)row * a.n_out + ch;
+    if ((a.n_out & 7) == 0) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     } else {
-      static_cast<__nv_bfloat16*>(a.out)[(size_t)row * a.n_out + ch] = __float2bfloat16_rn(f * y[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (ch + i < a.n_out) dst[i] = __float2bfloat16_rn(v[i]);
+    }
+    return;
+  }
+  const bool add = a.perm_token != nullptr;
+  const float s = add ? a.scale * a.row_gate[row] : 1.0f;
+  float* dst = static_cast<float*>(a.out) + (size_t)(add ? a.perm_token[row] : row) * a.n_out + ch;
+  if ((a.n_out & 7) == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 q = make_float4(s * v[i], s * v[i + 1], s * v[i + 2], s * v[i + 3]);
+      if (add) atomicAdd(reinterpret_cast<float4*>(dst + i), q);
+      else *reinterpret_cast<float4*>(dst + i) = q;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (ch + i >= a.n_out) break;
+      if (add) atomicAdd(dst + i, s * v[i]);
+      else dst[i] = v[i];
     }
   }
 }
 
-template <int NT, int CPS, bool SWIGLU>
+template <int NT, int CPS, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_mx4_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA64,
                const __grid_constant__ CUtensorMap tmA16, const Args g) {
@@ -282,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.tfull[i], 1);
-      mbar_init(&s.tempty[i], kEpiWarps * 32);
+      mbar_init(&s.tempty[i], kEpiWarps);
+      mbar_init(&s.sfull[i], kScaleWarps);
     }
     s.abort_flag = 0;
     fence_barrier_init();
@@ -362,44 +387,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ---- scales to TMEM and MMA ------------------------------------------------------------
+    // ---- MMA issuer --------------------------------------------------------------------------
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
-      long long it = 0;          // stages so far
+      int sl = 0;                // slot of scales
+      uint32_t sl_phase = 0;
       bool ok = true;
       for (int tile = blockIdx.x; ok && tile < total && !*abort_flag; tile += gridDim.x) {
         const Tile t = decode(s, g, tile, NT);
         const int npad = (t.n + 15) & ~15;
-        const int l0 = t.row0 - t.o_g;
-        const int sft = ((l0 & 127) + t.n + 127) / 128;
-        const uint32_t sft_col = (uint32_t)(l0 & 127) / 32u;
+        const uint32_t sft_col = (uint32_t)((t.row0 - t.o_g) & 127) / 32u;
         if (!mbar_wait(&s.tempty[acc], acc_phase ^ 1u, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * 2 * NT);
-        for (int kb = 0; kb < g.kstages; ++kb, ++it) {
-          if (!mbar_wait(&s.full[stage], phase, abort_flag)) { ok = false; break; }
-          // the slot's previous MMAs (two stages ago) have read their scales
-          if (it >= 2) {
-            const long long p = it - 2;
-            if (!mbar_wait(&s.empty[p % STAGES], (uint32_t)(p / STAGES) & 1u, abort_flag)) { ok = false; break; }
+        for (int kb = 0; kb < g.kstages; ++kb) {
+          if (!mbar_wait(&s.full[stage], phase, abort_flag) || !mbar_wait(&s.sfull[sl], sl_phase, abort_flag)) {
+            ok = false;
+            break;
           }
           tc_fence_after();
           const uint32_t w0 = smem_u32(s.ring[stage]);
           const uint32_t rows = w0 + 2 * W_BYTES;
-          const uint32_t sf = rows + C::T_BYTES;
-          const uint32_t slot = tmem + C::SF_COL + (uint32_t)(it & 1) * C::SF_SLOT;
-          const int pieces = min(CPS, g.chunks - kb * CPS);
-          for (int p = 0; p < pieces; ++p) {
-            tmem_cp_scales(slot + 4 * p, sf + p * 512);
-            if (t.blocks == 2) tmem_cp_scales(slot + CPS * 4 + 4 * p, sf + C::SFW_BYTES + p * 512);
-            for (int i = 0; i < sft; ++i)
-              tmem_cp_scales(slot + CPS * 8 + 8 * p + 4 * i, sf + (2 + i) * C::SFW_BYTES + p * 512);
-          }
-          const int ksteps = pieces * (4 / CPS);             // K = 64 each
-          for (int k = 0; k < ksteps; ++k) {
+          const uint32_t slot = tmem + C::SF_COL + (uint32_t)sl * C::SF_SLOT;
+          const int ksteps = min(CPS, g.chunks - kb * CPS) * (4 / CPS);      // K = 64 each
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k >= ksteps) break;
             const uint32_t p = k / (4 / CPS);
             const uint32_t idesc = idesc_mx4<NV>(npad, NV ? 0u : 2u * (k & 1));
             const uint64_t db = sw128_kmajor_desc(rows + k * 32);
@@ -411,6 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                            sfb, go);
           }
           umma_commit(&s.empty[stage]);
+          sl ^= 1;
+          if (sl == 0) sl_phase ^= 1u;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -422,15 +440,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (acc == 0) acc_phase ^= 1u;
       }
     }
+  } else if (warp >= 2 + kEpiWarps) {
+    // ---- scales: shared memory -> this warp's lane quarter of TMEM ----------------------------
+    const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+    int stage = 0;
+    uint32_t phase = 0;
+    int sl = 0;
+    // the stage before last, whose MMAs read the slot last
+    int before = STAGES - 2;
+    uint32_t before_phase = 1;   // the first two waits return at once
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      const Tile t = decode(s, g, tile, NT);
+      const int l0 = t.row0 - t.o_g;
+      const int sft = ((l0 & 127) + t.n + 127) / 128;
+      for (int kb = 0; kb < g.kstages; ++kb) {
+        // one lane waits, the warp follows it
+        int w_ok = 1;
+        if (lane == 0)
+          w_ok = mbar_wait(&s.full[stage], phase, abort_flag) &&
+                 mbar_wait(&s.empty[before], before_phase, abort_flag);
+        w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
+        if (!w_ok) { ok = false; break; }
+        tc_fence_after();
+        const uint8_t* sf = s.ring[stage] + 2 * W_BYTES + C::T_BYTES;
+        const uint32_t slot = tmem + quarter + C::SF_COL + (uint32_t)sl * C::SF_SLOT;
+        // pieces past the row's end hold an earlier stage's scales: written, never used
+        tmem_st_scales<CPS>(slot, 4, sf, lane);
+        if (t.blocks == 2) tmem_st_scales<CPS>(slot + CPS * 4, 4, sf + C::SFW_BYTES, lane);
+        for (int i = 0; i < sft; ++i)
+          tmem_st_scales<CPS>(slot + CPS * 8 + 4 * i, 8, sf + (2 + i) * C::SFW_BYTES, lane);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.sfull[sl]);
+        sl ^= 1;
+        if (++before == STAGES) {
+          before = 0;
+          before_phase ^= 1u;
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
   } else {
     // ---- epilogue: TMEM lane quarter = warp % 4; the two warps of a quarter take turns over
-    // groups of 8 columns ---------------------------------------------------------------------
+    // chunks of 16 columns ----------------------------------------------------------------------
     const int q = warp & 3;
     const int half = (warp - 2) >> 2;
     int acc = 0;
     uint32_t acc_phase = 0;
     const float af = NV && g.a_factor ? *g.a_factor : 1.0f;
-    const float hf = NV && SWIGLU && g.h_factor ? *g.h_factor : 1.0f;
+    const float hf = NV && MODE == kSwiglu && g.h_factor ? *g.h_factor : 1.0f;
+    const float inv6 = 1.0f / (6.0f * hf);
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
       const Tile t = decode(s, g, tile, NT);
       const float f = NV && g.w_factor ? af * g.w_factor[g.w_factor_per_group ? t.g : 0] : af;
@@ -440,22 +504,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!w_ok) break;
       tc_fence_after();
       const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 2 * NT);
+      const int ch = t.n0 + 32 * q + (lane & ~7);
 #pragma unroll 1
-      for (int c = 8 * half; c < t.n; c += 16) {
-        float v0[8], v1[8];
-        tmem_ld_32x32b_x8(base + c, v0);
-        if (t.blocks == 2) tmem_ld_32x32b_x8(base + NT + c, v1);
+      for (int c = 16 * half; c < t.n; c += 32) {
+        uint32_t v[2][16];
+        tmem_ld_32x32b_x16(base + c, v[0]);
+        tmem_ld_32x32b_x16(base + NT + c, v[1]);
         tmem_ld_wait();
-        if (SWIGLU) {
-          epi_swiglu<NV>(g, t, c, q, lane, f, v0, v1, hf);
-        } else {
-          epi_plain(g, t, c, t.n0 + 32 * q + lane, f, v0);
-          if (t.blocks == 2) epi_plain(g, t, c, t.n0 + 128 + 32 * q + lane, f, v1);
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+          float x[8];
+          if constexpr (MODE == kSwiglu) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float G = __uint_as_float(v[0][e + j]) * f, U = __uint_as_float(v[1][e + j]) * f;
+              x[j] = __fdividef(G, 1.0f + __expf(-G)) * U;
+            }
+            transpose8(x, lane);
+            epi_round_h<NV>(g, t, c + e, ch, lane, x, hf, inv6);
+            __syncwarp();
+          } else {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              if (b == t.blocks) break;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(v[b][e + j]);
+              transpose8(x, lane);
+              epi_store<MODE>(g, t, c + e, ch + 128 * b, lane, f, x);
+              __syncwarp();
+            }
+          }
         }
-        __syncwarp();
       }
       tc_fence_before();
-      mbar_arrive(&s.tempty[acc]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.tempty[acc]);
       if (C::ACCS == 2) acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -476,13 +559,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---- host side -------------------------------------------------------------------------------
-template <int NT, int CPS, bool SWIGLU>
+template <int NT, int CPS, int MODE>
 int launch_as(const CUtensorMap& w, const CUtensorMap& a64, const CUtensorMap& a16, const Args& g,
               int sm_count, cudaStream_t st) {
   using C = Cfg<NT, CPS>;
   constexpr size_t smem = sizeof(Storage<C::STAGES, C::STAGE>) + 1024;
   static_assert(smem <= 227 * 1024 && C::STAGES >= 3, "shared memory budget");
-  auto kern = k_mx4_gemm<NT, CPS, SWIGLU>;
+  auto kern = k_mx4_gemm<NT, CPS, MODE>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return MOE_ERR_CUDA;
   const cudaError_t e = launch_kernel(kern, sm_count, kThreads, smem, st, 1, w, a64, a16, g);
@@ -512,9 +595,10 @@ int launch_product(const moe_mx4_t& a, const moe_mx4_t& w, Args g, const DeviceI
   // Few rows per group on average: a tile of 64 rows leaves room for more stages of weights in
   // flight and a second accumulator. Else 192 rows, so that fewer tiles re-read the weights.
   const bool few = a.rows <= 64ll * a.groups;
-#define MX4_LAUNCH(NT, CPS) \
-  (swiglu ? launch_as<NT, CPS, true>(mw, a64, a16, g, dev.sm_count, st) \
-          : launch_as<NT, CPS, false>(mw, a64, a16, g, dev.sm_count, st))
+#define MX4_LAUNCH(NT, CPS)                                                                        \
+  (swiglu             ? launch_as<NT, CPS, kSwiglu>(mw, a64, a16, g, dev.sm_count, st)            \
+   : g.mode == kStore ? launch_as<NT, CPS, kStore>(mw, a64, a16, g, dev.sm_count, st)             \
+                      : launch_as<NT, CPS, kFp32>(mw, a64, a16, g, dev.sm_count, st))
   return is_nv(a) ? (few ? MX4_LAUNCH(64, 4) : MX4_LAUNCH(192, 4))
                : (few ? MX4_LAUNCH(64, 2) : MX4_LAUNCH(192, 2));
 #undef MX4_LAUNCH
@@ -579,9 +663,8 @@ int moe_mx4_grouped_gemm(const moe_mx4_t* a, const moe_mx4_t* w, void* out, int3
   DeviceInfo dev;
   MOE_TRY(current_device_info(&dev));
   Args g{};
-  g.mode = kStore;
+  g.mode = dtype == MOE_FP32 ? kFp32 : kStore;
   g.out = out;
-  g.out_fp32 = dtype == MOE_FP32;
   g.status = static_cast<int*>(ws);
   return launch_product(*a, *w, g, dev, as_stream(stream));
 }
@@ -626,9 +709,8 @@ int moe_mx4_grouped_ffn(const moe_mx4_t* a, const moe_mx4_t* w_gate_up, const mo
   g.status = static_cast<int*>(ws);
   MOE_TRY(launch_product(*a, *w_gate_up, g, dev, as_stream(stream)));
   Args d{};
-  d.mode = perm_token ? kAtomic : kStore;
+  d.mode = dtype == MOE_FP32 ? kFp32 : kStore;
   d.out = out;
-  d.out_fp32 = dtype == MOE_FP32;
   d.perm_token = perm_token;
   d.row_gate = row_gate;
   d.scale = scale;
