@@ -15,16 +15,16 @@
 //               weight boxes of 128 rows, the tile's rows in boxes of 64 and 16, and the block
 //               scales as plain bulk copies of the 512-byte pieces
 //   warp 1      TMEM owner and MMA issuer: 4 x 2 tcgen05.mma M128 K64 per stage
-//   warps 2-9   epilogue: tcgen05.ld, math, global stores
-//   warps 10-13 scales: each warp copies the stage's pieces from shared memory to its lane quarter
+//   warps 2-13  epilogue: tcgen05.ld, math, global stores
+//   warps 14-17 scales: each warp copies the stage's pieces from shared memory to its lane quarter
 //               of TMEM with tcgen05.st (the MMA reads them in all four quarters)
 // The scales of a stage alternate between two TMEM slots: before the scale warps overwrite a slot
 // they wait until the MMAs of two stages ago have completed. tcgen05.cp would copy them without
 // these warps, but each copy of 512 bytes holds up the tensor pipe for some 90 cycles (8 to 16
 // copies per stage of 768): 64 experts' gate/up at a decode batch took 214 us with it.
-// A lane of the epilogue reads one channel of 8 rows; an 8 x 8 transposition over 8 lanes gives it 8
-// channels of one row, so that it rounds h with one block scale and stores 16 or 32 bytes at once
-// (one channel per lane took 190 us of 750 at 32768 rows, in 2-byte stores).
+// A lane of the epilogue reads one channel of 8 rows; the warp turns them around in shared memory,
+// so that a lane has 8 channels of one row, rounds h with one block scale and stores 16 or 32 bytes
+// at once (one channel per lane took 190 us of 750 at 32768 rows, in 2-byte stores).
 //
 // Tiles: a group of `count` rows has ceil(count / NT) tiles along its rows; the table is built in
 // shared memory from `offsets` by every CTA, so the host never reads the counts. Columns past
@@ -44,10 +44,14 @@
 namespace moe {
 namespace {
 
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 12;                       // three per TMEM lane quarter
 constexpr int kScaleWarps = 4;
 constexpr int kThreads = 64 + (kEpiWarps + kScaleWarps) * 32;
 constexpr uint32_t kTmemCols = 512;
+// a warp's staging rows: 8 rows of 32 channels, 4 floats apart from a multiple of 32, so that
+// neither the writes (a row at a time) nor the reads (16 bytes of 8 rows) meet in a bank
+constexpr int kStageLd = 36;
+constexpr int kEpiBytes = kEpiWarps * 8 * kStageLd * 4;
 constexpr int W_BYTES = 128 * 128;                  // a weight block's stage: 128 rows x 128 bytes
 
 // kStore: y in bf16; kFp32: y in fp32, stored or added to the tokens' sums; kSwiglu: h in 4 bits
@@ -84,7 +88,7 @@ struct Cfg {
   static constexpr int SFT_TILES = NT > 64 ? 2 : 1;       // 128-row scale tiles that NT rows span
   static constexpr int SFW_BYTES = CPS * 512;
   static constexpr int STAGE = 2 * W_BYTES + T_BYTES + (2 + SFT_TILES) * SFW_BYTES;
-  static constexpr int STAGES = (227 * 1024 - 12 * 1024) / STAGE;
+  static constexpr int STAGES = (227 * 1024 - 12 * 1024 - kEpiBytes) / STAGE;
   static constexpr int ACCS = NT > 64 ? 1 : 2;            // accumulator sets of 2 NT columns
   static constexpr int SF_COL = ACCS * 2 * NT;            // TMEM columns of the scales' slots
   static constexpr int SF_SLOT = CPS * 16;                // W0: CPS x 4, W1: CPS x 4, rows: CPS x 8
@@ -104,6 +108,7 @@ struct alignas(1024) Storage {
   int abort_flag;
   int offs[kMx4MaxGroups + 1];
   int toff[kMx4MaxGroups + 1];
+  alignas(16) float turn[kEpiWarps][8][kStageLd];
 };
 
 struct Tile {
@@ -195,20 +200,17 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// 8 x 8 transposition over the lanes of each 8-lane group: lane i's v[j] goes to lane j's v[i].
-__device__ __forceinline__ void transpose8(float (&v)[8], int lane) {
+// The warp's 32 channels (one per lane) of 8 rows, v[j] of row j, turned around: afterwards v[i]
+// is channel 8 (lane / 8) + i of row lane % 8.
+__device__ __forceinline__ void turn_around(float (&v)[8], float (*stg)[kStageLd], int lane) {
 #pragma unroll
-  for (int s = 4; s > 0; s >>= 1) {
-    const bool upper = lane & s;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i & s) continue;
-      const float keep = upper ? v[i + s] : v[i];
-      const float got = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + s], s);
-      v[i] = upper ? got : keep;
-      v[i + s] = upper ? keep : got;
-    }
-  }
+  for (int j = 0; j < 8; ++j) stg[j][lane] = v[j];
+  __syncwarp();
+  const float4* p = reinterpret_cast<const float4*>(&stg[lane & 7][lane & 24]);
+  const float4 a = p[0], b = p[1];
+  __syncwarp();                // the rows may be written again
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
 // ---- epilogues: 8 rows of the tile from row c on; v: 8 channels, from channel ch on, of row
@@ -486,10 +488,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---- epilogue: TMEM lane quarter = warp % 4; the two warps of a quarter take turns over
+    // ---- epilogue: TMEM lane quarter = warp % 4; the three warps of a quarter take turns over
     // chunks of 16 columns ----------------------------------------------------------------------
     const int q = warp & 3;
-    const int half = (warp - 2) >> 2;
+    const int third = (warp - 2) >> 2;
+    float (*stg)[kStageLd] = s.turn[warp - 2];
     int acc = 0;
     uint32_t acc_phase = 0;
     const float af = NV && g.a_factor ? *g.a_factor : 1.0f;
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 2 * NT);
       const int ch = t.n0 + 32 * q + (lane & ~7);
 #pragma unroll 1
-      for (int c = 16 * half; c < t.n; c += 32) {
+      for (int c = 16 * third; c < t.n; c += 16 * (kEpiWarps / 4)) {
         uint32_t v[2][16];
         tmem_ld_32x32b_x16(base + c, v[0]);
         tmem_ld_32x32b_x16(base + NT + c, v[1]);
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float G = __uint_as_float(v[0][e + j]) * f, U = __uint_as_float(v[1][e + j]) * f;
               x[j] = __fdividef(G, 1.0f + __expf(-G)) * U;
             }
-            transpose8(x, lane);
+            turn_around(x, stg, lane);
             epi_round_h<NV>(g, t, c + e, ch, lane, x, hf, inv6);
             __syncwarp();
           } else {
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (b == t.blocks) break;
 #pragma unroll
               for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(v[b][e + j]);
-              transpose8(x, lane);
+              turn_around(x, stg, lane);
               epi_store<MODE>(g, t, c + e, ch + 128 * b, lane, f, x);
               __syncwarp();
             }
