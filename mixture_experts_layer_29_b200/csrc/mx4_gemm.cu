@@ -10,16 +10,29 @@
 // weight blocks of 128 rows, which share the tile's rows: the gate and up rows of the same 128
 // channels of h, or 256 outputs of a plain product. TMEM lane = output channel, column = row.
 //
-// Kernel structure (one CTA per SM, persistent, static round-robin over tiles):
-//   warp 0      TMA producer: per stage of K = 256 elements (128 bytes, 128-byte swizzle) two
-//               weight boxes of 128 rows, the tile's rows in boxes of 64 and 16, and the block
-//               scales as plain bulk copies of the 512-byte pieces
-//   warp 1      TMEM owner and MMA issuer: 4 x 2 tcgen05.mma M128 K64 per stage
-//   warps 2-13  epilogue: tcgen05.ld, math, global stores
-//   warps 14-17 scales: each warp copies the stage's pieces from shared memory to its lane quarter
+// Two kernels, both persistent with a static round-robin over tiles:
+//  * k_mx4_gemm, one CTA per SM, for few rows per group: a tile is two blocks of 128 weight rows
+//    (the gate and up rows of 128 channels of h, or 256 outputs of a plain product) by up to 64
+//    rows of the group. Bound by streaming the weights.
+//  * k_mx4_gemm_pair, CTA pairs (cta_group::2), for many rows: a tile is 256 weight rows, 128 per
+//    CTA (64 gate and the same 64 up rows, or 128 outputs), by up to 192 rows of the group, half
+//    of which each CTA holds. An e2m1 MMA of one CTA reads both operands from its shared memory
+//    at about the rate that memory has (107 bytes a cycle at N = 192 besides what TMA writes); in
+//    a pair each CTA reads half of the rows. Two accumulators let the epilogue of a tile overlap
+//    the MMAs of the next.
+// Warps:
+//   0           TMA producer: per stage of K = 256 elements (128 bytes, 128-byte swizzle) the
+//               weight boxes, the tile's rows in a few boxes, and (in the pair kernel a warp of
+//               its own, 18) the block scales as plain bulk copies of the 512-byte pieces
+//   1           TMEM owner and MMA issuer (the pair's leader): 4 tcgen05.mma of K = 64 per stage
+//               and weight block
+//   2-13        epilogue: tcgen05.ld, math, global stores
+//   14-17       scales: each warp copies the stage's pieces from shared memory to its lane quarter
 //               of TMEM with tcgen05.st (the MMA reads them in all four quarters)
-// The scales of a stage alternate between two TMEM slots: before the scale warps overwrite a slot
-// they wait until the MMAs of two stages ago have completed. tcgen05.cp would copy them without
+// The scales of the stages take turns over the TMEM columns that are left, 3 to 5 slots: with fewer
+// slots than stages the scale warps wait, before they overwrite a slot, until the MMAs that read it
+// have completed. (Two slots held the pair kernel up: from one MMA's end to the next scales in TMEM
+// takes about as long as a stage's MMAs; 594 us instead of 390 at 32768 rows.) tcgen05.cp would copy them without
 // these warps, but each copy of 512 bytes holds up the tensor pipe for some 90 cycles (8 to 16
 // copies per stage of 768): 64 experts' gate/up at a decode batch took 214 us with it.
 // A lane of the epilogue reads one channel of 8 rows; the warp turns them around in shared memory,
@@ -34,6 +47,7 @@
 #include <cudaTypedefs.h>
 
 #include <cstddef>
+#include <mutex>
 
 #include "checks.cuh"
 #include "common.cuh"
@@ -47,11 +61,16 @@ namespace {
 constexpr int kEpiWarps = 12;                       // three per TMEM lane quarter
 constexpr int kScaleWarps = 4;
 constexpr int kThreads = 64 + (kEpiWarps + kScaleWarps) * 32;
+constexpr int kScaleProducer = 2 + kEpiWarps + kScaleWarps;    // pair kernel: a warp more
+constexpr int kPairThreads = kThreads + 32;
 constexpr uint32_t kTmemCols = 512;
 // a warp's staging rows: 8 rows of 32 channels, 4 floats apart from a multiple of 32, so that
 // neither the writes (a row at a time) nor the reads (16 bytes of 8 rows) meet in a bank
 constexpr int kStageLd = 36;
-constexpr int kEpiBytes = kEpiWarps * 8 * kStageLd * 4;
+constexpr int kGroupLd = 132;
+constexpr int kEpiFloats = kEpiWarps / 4 * 16 * kGroupLd;
+constexpr int kEpiBytes = kEpiFloats * 4;
+static_assert(kEpiFloats >= kEpiWarps * 8 * kStageLd, "staging rows");
 constexpr int W_BYTES = 128 * 128;                  // a weight block's stage: 128 rows x 128 bytes
 
 // kStore: y in bf16; kFp32: y in fp32, stored or added to the tokens' sums; kSwiglu: h in 4 bits
@@ -80,40 +99,57 @@ struct Args {
   int* status;
 };
 
-// NT: rows of a tile. CPS: scale pieces of a stage along K (2: MXFP4, 4: NVFP4).
-template <int NT, int CPS>
-struct Cfg {
-  static constexpr bool kNv = CPS == 4;
+// CPS: scale pieces of a stage along K (2: MXFP4, 4: NVFP4); NT: rows of a tile
+template <int CPS>
+struct One {
+  static constexpr int NT = 64;
   static constexpr int T_BYTES = NT * 128;
-  static constexpr int SFT_TILES = NT > 64 ? 2 : 1;       // 128-row scale tiles that NT rows span
-  static constexpr int SFW_BYTES = CPS * 512;
-  static constexpr int STAGE = 2 * W_BYTES + T_BYTES + (2 + SFT_TILES) * SFW_BYTES;
+  static constexpr int SF_BYTES = CPS * 512;               // a stage's pieces of 128 rows
+  static constexpr int STAGE = 2 * W_BYTES + T_BYTES + 3 * SF_BYTES;   // two weight blocks, the rows
   static constexpr int STAGES = (227 * 1024 - 12 * 1024 - kEpiBytes) / STAGE;
-  static constexpr int ACCS = NT > 64 ? 1 : 2;            // accumulator sets of 2 NT columns
-  static constexpr int SF_COL = ACCS * 2 * NT;            // TMEM columns of the scales' slots
-  static constexpr int SF_SLOT = CPS * 16;                // W0: CPS x 4, W1: CPS x 4, rows: CPS x 8
+  static constexpr int SF_COL = 4 * NT;                    // after two accumulators of two blocks
+  static constexpr int SF_SLOT = CPS * 10;                 // W0: CPS x 4, W1: CPS x 4, rows: CPS x 2
+  static constexpr int SLOTS = STAGES;
   static_assert(STAGE % 1024 == 0, "128-byte-swizzled boxes need 1024-byte alignment");
-  static_assert(SF_COL + 2 * SF_SLOT <= (int)kTmemCols, "TMEM budget");
+  static_assert(SF_COL + SLOTS * SF_SLOT <= (int)kTmemCols, "TMEM budget");
+};
+template <int CPS>
+struct Pair {
+  static constexpr int NT = 192;
+  static constexpr int T_BYTES = NT / 2 * 128;             // this CTA's half of the rows
+  static constexpr int SF_BYTES = CPS * 512;
+  static constexpr int STAGE = W_BYTES + T_BYTES + 4 * SF_BYTES;       // gate and up (or W), the rows: two
+  static constexpr int STAGES = (227 * 1024 - 12 * 1024 - kEpiBytes) / STAGE;
+  static constexpr int SF_COL = 2 * NT;                    // after two accumulators
+  static constexpr int SF_SLOT = CPS * 10;                 // W: CPS x 4, rows: CPS x 6
+  static constexpr int FIT = ((int)kTmemCols - SF_COL) / SF_SLOT;
+  static constexpr int SLOTS = FIT < STAGES ? FIT : STAGES;
+  static_assert(STAGE % 1024 == 0, "128-byte-swizzled boxes need 1024-byte alignment");
+  static_assert(SLOTS >= 3, "TMEM budget");
 };
 
-template <int STAGES, int STAGE>
+template <class C>
 struct alignas(1024) Storage {
-  uint8_t ring[STAGES][STAGE];
-  uint64_t full[STAGES];
-  uint64_t empty[STAGES];
+  uint8_t ring[C::STAGES][C::STAGE];
+  uint64_t full[C::STAGES];   // operands (pair: of both CTAs, on the leader) have landed
+  uint64_t sland[C::STAGES];  // pair: this CTA's scales have landed
+  uint64_t empty[C::STAGES];
   uint64_t tfull[2];
   uint64_t tempty[2];
-  uint64_t sfull[2];        // a slot of scales is in TMEM
+  uint64_t sfull[C::SLOTS];   // a slot of scales is in TMEM (pair: of both CTAs, on the leader)
   uint32_t tmem_base;
   int abort_flag;
   int offs[kMx4MaxGroups + 1];
   int toff[kMx4MaxGroups + 1];
-  alignas(16) float turn[kEpiWarps][8][kStageLd];
+  int turn_ok[kEpiWarps];     // the warps of a channel range tell each other whether to go on
+  // staging rows of the epilogue: [warp][8][kStageLd], or [four warps][16][kGroupLd] where the
+  // warps of a channel range work together
+  alignas(16) float turn[kEpiFloats];
 };
 
 struct Tile {
-  int g, row0, row_end, o_g, n0, n;   // n: rows of the tile
-  int blocks;                         // weight blocks of 128 rows: 1 or 2
+  int g, row0, row_end, o_g, n0, n;   // n: rows of the tile, n0: its first channel
+  int blocks;                         // one CTA: weight blocks of 128 rows, 1 or 2
 };
 
 // Tile order: group by group, inside a group channel tile by channel tile with the row tiles
@@ -135,25 +171,27 @@ __device__ __forceinline__ Tile decode(const S& s, const Args& g, int tile, int 
   t.row0 = t.o_g + (l - nt * rt) * NT;
   t.row_end = s.offs[lo + 1];
   t.n = min(NT, t.row_end - t.row0);
-  const int per = g.mode == kSwiglu ? 128 : 256;
-  t.n0 = nt * per;
+  t.n0 = nt * (g.mode == kSwiglu ? 128 : 256);
   t.blocks = g.mode == kSwiglu || t.n0 + 128 < g.n_out ? 2 : 1;
   return t;
 }
 
 // ---- tcgen05 with block scales ---------------------------------------------------------------
+__device__ __forceinline__ void tmem_st_x4(uint32_t taddr, const uint4& v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_x2(uint32_t taddr, uint32_t a, uint32_t b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(a), "r"(b) : "memory");
+}
 // P pieces of scales (512 bytes each, one after another) -> 4 P TMEM columns from taddr on, this
-// warp's lane quarter: lane l holds bytes [16 l, 16 l + 16) of each piece. `step` is the distance
-// of the pieces' columns.
+// warp's lane quarter: lane l holds bytes [16 l, 16 l + 16) of each piece.
 template <int P>
-__device__ __forceinline__ void tmem_st_scales(uint32_t taddr, int step, const uint8_t* pieces, int lane) {
+__device__ __forceinline__ void tmem_st_scales(uint32_t taddr, const uint8_t* pieces, int lane) {
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const uint4 v = *reinterpret_cast<const uint4*>(pieces + p * 512 + lane * 16);
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr + p * step),
-                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-  }
+  for (int p = 0; p < P; ++p)
+    tmem_st_x4(taddr + 4 * p, *reinterpret_cast<const uint4*>(pieces + p * 512 + lane * 16));
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -182,13 +220,37 @@ __device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uin
   }
 }
 
+// The same by a CTA pair, issued by its leader: M = 256, 128 rows of A and N / 2 of B per CTA; each
+// CTA's TMEM holds the scales of its rows of A and of all N rows of B.
+template <bool NV>
+__device__ __forceinline__ void umma_mx4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                              uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if (NV) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  }
+}
+
 // Instruction descriptor, block-scaled 4-bit kinds: A and B e2m1 (bits 7-9 and 10-11 = 1), both
 // K-major, N >> 3 in bits 17-22, scale type in bit 23 (1: e8m0, 0: e4m3), M >> 7 in bits 27-28;
 // the byte of the scales' 32-bit columns that the MMA starts at: bits 4-5 (B), 29-30 (A).
 template <bool NV>
-__device__ __forceinline__ uint32_t idesc_mx4(int N, uint32_t sf_id) {
+__device__ __forceinline__ uint32_t idesc_mx4(int M, int N, uint32_t sf_id) {
   return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (NV ? 0u : (1u << 23)) |
-         (1u << 27) | (sf_id << 4) | (sf_id << 29);
+         (static_cast<uint32_t>(M >> 7) << 27) | (sf_id << 4) | (sf_id << 29);
 }
 
 // Untiled bulk copy global -> shared, completion counted on `bar`; 16-byte aligned both sides.
@@ -213,11 +275,24 @@ __device__ __forceinline__ void turn_around(float (&v)[8], float (*stg)[kStageLd
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
+// The scale byte of a block of h with the largest magnitude top (as bits) and what its values are
+// multiplied by before rounding (0: they all round to 0). hf: h's factor, inv6 = 1 / (6 hf). h comes
+// out of an fp32 accumulation, so NVFP4 divides by way of reciprocals here: that moves h by two
+// units in its last place at most.
+template <bool NV>
+__device__ __forceinline__ uint32_t round_scale(uint32_t top, float hf, float inv6, float& by) {
+  if (!NV) return mx4_scale<false>(top, 1.0f, by);
+  by = 0.f;
+  if (top >= 0x7F800000u) return 0x7Fu;
+  const uint32_t byte = e4m3(__uint_as_float(top) * inv6);
+  if (byte != 0u) by = 1.0f / (e4m3_value(byte) * hf);
+  return byte;
+}
+__device__ __forceinline__ float scaled_h(float h, float by) { return by != 0.f ? h * by : 0.f; }
+
 // ---- epilogues: 8 rows of the tile from row c on; v: 8 channels, from channel ch on, of row
 // c + lane % 8 ------------------------------------------------------------------------------
 // h rounded to 4 bits: the warp's 32 channels are one (MXFP4) or two (NVFP4) blocks of each row.
-// hf: h's factor, inv6 = 1 / (6 hf). h comes out of an fp32 accumulation, so NVFP4 divides by way
-// of reciprocals here: that moves h by two units in its last place at most.
 template <bool NV>
 __device__ __forceinline__ void epi_round_h(const Args& a, const Tile& t, int c, int ch, int lane,
                                             const float (&h)[8], float hf, float inv6) {
@@ -226,18 +301,12 @@ __device__ __forceinline__ void epi_round_h(const Args& a, const Tile& t, int c,
   for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
   if (!NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-  float by = 0.f;
-  uint32_t byte;
-  if (NV) {
-    byte = top >= 0x7F800000u ? 0x7Fu : e4m3(__uint_as_float(top) * inv6);
-    if (top < 0x7F800000u && byte != 0u) by = 1.0f / (e4m3_value(byte) * hf);
-  } else {
-    byte = mx4_scale<false>(top, 1.0f, by);
-  }
+  float by;
+  const uint32_t byte = round_scale<NV>(top, hf, inv6, by);
   uint32_t v = 0;
 #pragma unroll
   for (int i = 0; i < 8; i += 2)
-    v |= e2m1x2(by != 0.f ? h[i] * by : 0.f, by != 0.f ? h[i + 1] * by : 0.f) << (4 * i);
+    v |= e2m1x2(scaled_h(h[i], by), scaled_h(h[i + 1], by)) << (4 * i);
   const int j = lane & 7;
   if (c + j >= t.n) return;
   const int row = t.row0 + c + j;
@@ -288,44 +357,14 @@ __device__ __forceinline__ void epi_store(const Args& a, const Tile& t, int c, i
   }
 }
 
-template <int NT, int CPS, int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_mx4_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA64,
-               const __grid_constant__ CUtensorMap tmA16, const Args g) {
-  using C = Cfg<NT, CPS>;
-  constexpr bool NV = C::kNv;
-  constexpr int STAGES = C::STAGES;
-  extern __shared__ uint8_t smem_raw[];
-  auto& s = *reinterpret_cast<Storage<STAGES, C::STAGE>*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch_dependents();
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.tfull[i], 1);
-      mbar_init(&s.tempty[i], kEpiWarps);
-      mbar_init(&s.sfull[i], kScaleWarps);
-    }
-    s.abort_flag = 0;
-    fence_barrier_init();
-    prefetch_tensormap(&tmW);
-    prefetch_tensormap(&tmA64);
-    prefetch_tensormap(&tmA16);
-  }
-  if (warp == 1) {
-    tmem_alloc(&s.tmem_base, kTmemCols);
-    tmem_relinquish();
-  }
-  pdl_wait();
-  for (int i = threadIdx.x; i <= g.a.groups; i += kThreads) s.offs[i] = g.a.begin(i);
+// The tables of the groups' rows and row tiles, by every thread of the CTA.
+template <class S>
+__device__ __forceinline__ void build_table(S& s, const Args& g, int NT) {
+  for (int i = threadIdx.x; i <= g.a.groups; i += blockDim.x) s.offs[i] = g.a.begin(i);
   __syncthreads();
-  if (warp == 2) {
+  if (threadIdx.x >= 64 && threadIdx.x < 96) {
     // toff[e] = sum over e' < e of ceil(count_e' / NT)
+    const int lane = threadIdx.x & 31;
     const int per = (g.a.groups + 31) / 32;
     const int b = lane * per;
     auto tiles_of = [&](int e) { return (s.offs[e + 1] - s.offs[e] + NT - 1) / NT; };
@@ -341,6 +380,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     if (lane == 31) s.toff[g.a.groups] = inc;
   }
+}
+
+// The first scale pieces of the 128-row tile of group g that has its row l.
+__device__ __forceinline__ const uint8_t* scale_tile(const uint8_t* scales, int64_t o_g, int g, int l, int chunks) {
+  return scales + ((size_t)(o_g >> 7) + g + (l >> 7)) * chunks * 512;
+}
+
+template <int CPS, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_mx4_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA64,
+               const __grid_constant__ CUtensorMap tmA16, const Args g) {
+  using C = One<CPS>;
+  constexpr bool NV = CPS == 4;
+  constexpr int STAGES = C::STAGES, NT = C::NT;
+  extern __shared__ uint8_t smem_raw[];
+  auto& s = *reinterpret_cast<Storage<C>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.tfull[i], 1);
+      mbar_init(&s.tempty[i], kEpiWarps);
+    }
+    for (int i = 0; i < C::SLOTS; ++i) mbar_init(&s.sfull[i], kScaleWarps);
+    s.abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmA64);
+    prefetch_tensormap(&tmA16);
+  }
+  if (warp == 1) {
+    tmem_alloc(&s.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  build_table(s, g, NT);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -356,31 +437,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int tile = blockIdx.x; tile < total && !*abort_flag; tile += gridDim.x) {
         const Tile t = decode(s, g, tile, NT);
         const int big = t.n / 64, small = (t.n % 64 + 15) / 16;
-        const int l0 = t.row0 - t.o_g;
-        const int sft = ((l0 & 127) + t.n + 127) / 128;      // scale tiles of the rows
         const int wrow = t.g * g.w_rows + t.n0;
-        const size_t wtile = (size_t)((t.g * (int64_t)g.w_rows) >> 7) + t.g;
-        const uint8_t* sw = g.w_scales + (wtile + t.n0 / 128) * g.chunks * 512;
-        const uint8_t* sw2 = sw + (size_t)(g.w_second / 128) * g.chunks * 512;
-        const uint8_t* sa = g.a_scales + ((size_t)(t.o_g >> 7) + t.g + (l0 >> 7)) * g.chunks * 512;
+        const int64_t wo = (int64_t)t.g * g.w_rows;
+        const uint8_t* sw = scale_tile(g.w_scales, wo, t.g, t.n0, g.chunks);
+        const uint8_t* sw2 = scale_tile(g.w_scales, wo, t.g, t.n0 + g.w_second, g.chunks);
+        const uint8_t* sa = scale_tile(g.a_scales, t.o_g, t.g, t.row0 - t.o_g, g.chunks);
         for (int kb = 0; kb < g.kstages; ++kb) {
           if (!mbar_wait(&s.empty[stage], phase ^ 1u, abort_flag)) break;
           uint8_t* st = s.ring[stage];
           uint64_t* bar = &s.full[stage];
           const uint32_t sfb = 512u * (uint32_t)min(CPS, g.chunks - kb * CPS);
-          mbar_arrive_expect_tx(bar, t.blocks * (W_BYTES + sfb) + (big * 64 + small * 16) * 128 + sft * sfb);
+          mbar_arrive_expect_tx(bar, t.blocks * (W_BYTES + sfb) + (big * 64 + small * 16) * 128 + sfb);
           tma_load_2d(st, &tmW, kb * 128, wrow, bar);
           if (t.blocks == 2) tma_load_2d(st + W_BYTES, &tmW, kb * 128, wrow + g.w_second, bar);
           uint8_t* rows = st + 2 * W_BYTES;
-          for (int i = 0; i < big; ++i) tma_load_2d(rows + i * 64 * 128, &tmA64, kb * 128, t.row0 + i * 64, bar);
+          if (big) tma_load_2d(rows, &tmA64, kb * 128, t.row0, bar);
           for (int i = 0; i < small; ++i)
             tma_load_2d(rows + (big * 64 + i * 16) * 128, &tmA16, kb * 128, t.row0 + big * 64 + i * 16, bar);
           uint8_t* sf = rows + C::T_BYTES;
           const size_t at = (size_t)kb * CPS * 512;
           bulk_load(sf, sw + at, sfb, bar);
-          if (t.blocks == 2) bulk_load(sf + C::SFW_BYTES, sw2 + at, sfb, bar);
-          for (int i = 0; i < sft; ++i)
-            bulk_load(sf + (2 + i) * C::SFW_BYTES, sa + (size_t)i * g.chunks * 512 + at, sfb, bar);
+          if (t.blocks == 2) bulk_load(sf + C::SF_BYTES, sw2 + at, sfb, bar);
+          bulk_load(sf + 2 * C::SF_BYTES, sa + at, sfb, bar);     // 64 rows lie in one scale tile
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -401,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int tile = blockIdx.x; ok && tile < total && !*abort_flag; tile += gridDim.x) {
         const Tile t = decode(s, g, tile, NT);
         const int npad = (t.n + 15) & ~15;
-        const uint32_t sft_col = (uint32_t)((t.row0 - t.o_g) & 127) / 32u;
         if (!mbar_wait(&s.tempty[acc], acc_phase ^ 1u, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * 2 * NT);
@@ -419,9 +496,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k) {
             if (k >= ksteps) break;
             const uint32_t p = k / (4 / CPS);
-            const uint32_t idesc = idesc_mx4<NV>(npad, NV ? 0u : 2u * (k & 1));
+            const uint32_t idesc = idesc_mx4<NV>(128, npad, NV ? 0u : 2u * (k & 1));
             const uint64_t db = sw128_kmajor_desc(rows + k * 32);
-            const uint32_t sfb = slot + CPS * 8 + 8 * p + sft_col;
+            const uint32_t sfb = slot + CPS * 8 + 2 * p;
             const uint32_t go = (kb > 0 || k > 0) ? 1u : 0u;
             umma_mx4<NV>(d, sw128_kmajor_desc(w0 + k * 32), db, idesc, slot + 4 * p, sfb, go);
             if (t.blocks == 2)
@@ -429,8 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                            sfb, go);
           }
           umma_commit(&s.empty[stage]);
-          sl ^= 1;
-          if (sl == 0) sl_phase ^= 1u;
+          if (++sl == C::SLOTS) {
+            sl = 0;
+            sl_phase ^= 1u;
+          }
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -438,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         umma_commit(&s.tfull[acc]);
-        if (C::ACCS == 2) acc ^= 1;
+        acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
     }
@@ -448,39 +527,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     int sl = 0;
-    // the stage before last, whose MMAs read the slot last
-    int before = STAGES - 2;
-    uint32_t before_phase = 1;   // the first two waits return at once
     bool ok = true;
     for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
       const Tile t = decode(s, g, tile, NT);
-      const int l0 = t.row0 - t.o_g;
-      const int sft = ((l0 & 127) + t.n + 127) / 128;
+      const int upper = ((t.row0 - t.o_g) & 64) / 8;         // the rows' half of their scale tile
       for (int kb = 0; kb < g.kstages; ++kb) {
         // one lane waits, the warp follows it
         int w_ok = 1;
-        if (lane == 0)
-          w_ok = mbar_wait(&s.full[stage], phase, abort_flag) &&
-                 mbar_wait(&s.empty[before], before_phase, abort_flag);
+        if (lane == 0) w_ok = mbar_wait(&s.full[stage], phase, abort_flag) ? 1 : 0;
         w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
         if (!w_ok) { ok = false; break; }
         tc_fence_after();
         const uint8_t* sf = s.ring[stage] + 2 * W_BYTES + C::T_BYTES;
         const uint32_t slot = tmem + quarter + C::SF_COL + (uint32_t)sl * C::SF_SLOT;
         // pieces past the row's end hold an earlier stage's scales: written, never used
-        tmem_st_scales<CPS>(slot, 4, sf, lane);
-        if (t.blocks == 2) tmem_st_scales<CPS>(slot + CPS * 4, 4, sf + C::SFW_BYTES, lane);
-        for (int i = 0; i < sft; ++i)
-          tmem_st_scales<CPS>(slot + CPS * 8 + 4 * i, 8, sf + (2 + i) * C::SFW_BYTES, lane);
+        tmem_st_scales<CPS>(slot, sf, lane);
+        if (t.blocks == 2) tmem_st_scales<CPS>(slot + CPS * 4, sf + C::SF_BYTES, lane);
+#pragma unroll
+        for (int p = 0; p < CPS; ++p) {
+          const uint2 v = *reinterpret_cast<const uint2*>(sf + 2 * C::SF_BYTES + p * 512 + lane * 16 + upper);
+          tmem_st_x2(slot + CPS * 8 + 2 * p, v.x, v.y);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.sfull[sl]);
-        sl ^= 1;
-        if (++before == STAGES) {
-          before = 0;
-          before_phase ^= 1u;
-        }
+        if (++sl == C::SLOTS) sl = 0;
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -492,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // chunks of 16 columns ----------------------------------------------------------------------
     const int q = warp & 3;
     const int third = (warp - 2) >> 2;
-    float (*stg)[kStageLd] = s.turn[warp - 2];
+    float (*stg)[kStageLd] = reinterpret_cast<float (*)[kStageLd]>(s.turn + (warp - 2) * 8 * kStageLd);
     int acc = 0;
     uint32_t acc_phase = 0;
     const float af = NV && g.a_factor ? *g.a_factor : 1.0f;
@@ -542,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.tempty[acc]);
-      if (C::ACCS == 2) acc ^= 1;
+      acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
   }
@@ -561,17 +633,415 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ---- CTA pairs ---------------------------------------------------------------------------------
+// h of the pair kernel, where lanes 0-63 hold the gate and 64-127 the up rows of the CTA's 64
+// channels: the four warps of a channel range (one per lane quarter) have staged 16 rows from c on
+// as S[row][TMEM lane]; this warp takes rows 4 q to 4 q + 3, two at a time, 4 channels per lane.
+// ch: the CTA's first channel.
+template <bool NV>
+__device__ __forceinline__ void epi_round_h_pair(const Args& a, const Tile& t, int c, int ch, int q, int lane, float f,
+                                                 const float (*S)[kGroupLd], float hf, float inv6) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    const int r = 4 * q + e + (lane >> 4), k = 4 * (lane & 15);
+    const float4 G = *reinterpret_cast<const float4*>(&S[r][k]);
+    const float4 U = *reinterpret_cast<const float4*>(&S[r][64 + k]);
+    const float gv[4] = {G.x, G.y, G.z, G.w}, uv[4] = {U.x, U.y, U.z, U.w};
+    float h[4];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = gv[i] * f;
+      h[i] = __fdividef(x, 1.0f + __expf(-x)) * (uv[i] * f);
+      top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+    }
+#pragma unroll
+    for (int o = 1; o < mx4_block(NV) / 4; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float by;
+    const uint32_t byte = round_scale<NV>(top, hf, inv6, by);
+    const uint32_t v = e2m1x2(scaled_h(h[0], by), scaled_h(h[1], by)) | e2m1x2(scaled_h(h[2], by), scaled_h(h[3], by)) << 8;
+    if (c + r < t.n) {
+      const int row = t.row0 + c + r;
+      *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.out) + (size_t)row * (a.n_out / 2) + (ch + k) / 2) = (uint16_t)v;
+      if (k % mx4_block(NV) == 0)
+        a.h_scales[mx4_scale_at(t.o_g, t.g, row - t.o_g, (ch + k) / mx4_block(NV), a.n_out / (4 * mx4_block(NV)))] =
+            (uint8_t)byte;
+    }
+    __syncwarp();
+  }
+}
+
+// The epilogue warps of one channel range (four warps) meet here; named barriers 1 to 3.
+__device__ __forceinline__ void range_bar(int third) { asm volatile("bar.sync %0, 128;" ::"r"(third + 1) : "memory"); }
+
+template <int CPS, int MODE>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    k_mx4_gemm_pair(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW64,
+                    const __grid_constant__ CUtensorMap tmA96, const __grid_constant__ CUtensorMap tmA16, const Args g) {
+  using C = Pair<CPS>;
+  constexpr bool NV = CPS == 4;
+  constexpr int STAGES = C::STAGES, NT = C::NT;
+  extern __shared__ uint8_t smem_raw[];
+  auto& s = *reinterpret_cast<Storage<C>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();            // 0: leader, 1: peer
+  const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  pdl_launch_dependents();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.sland[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.tfull[i], 1);
+      mbar_init(&s.tempty[i], 2 * kEpiWarps);
+    }
+    for (int i = 0; i < C::SLOTS; ++i) mbar_init(&s.sfull[i], 2 * kScaleWarps);
+    s.abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(MODE == kSwiglu ? &tmW64 : &tmW);
+    prefetch_tensormap(&tmA96);
+    prefetch_tensormap(&tmA16);
+  }
+  pdl_wait();
+  __syncthreads();
+  cluster_sync();                                     // both CTAs' barriers initialised
+  if (warp == 1) {
+    tmem_alloc_pair(&s.tmem_base, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  build_table(s, g, NT);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  const int total = s.toff[g.a.groups] * g.n_tiles;
+  volatile int* abort_flag = &s.abort_flag;
+
+  if (warp == 0) {
+    // ---- TMA producer of the operands (both CTAs), counted on the leader -----------------------
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int tile = cluster; tile < total && !*abort_flag; tile += nclusters) {
+        const Tile t = decode(s, g, tile, NT);
+        const int mine = ((t.n + 31) & ~31) / 2;             // rows of this CTA's half
+        const int arow = t.row0 + mine * (int)rank;
+        // this CTA's first weight row; past the group's end (an odd number of 128-row blocks)
+        // the boxes read on or are zeros: those channels are dropped
+        const int wrow = t.g * g.w_rows + t.n0 + (MODE == kSwiglu ? 64 : 128) * (int)rank;
+        for (int kb = 0; kb < g.kstages; ++kb) {
+          if (!mbar_wait(&s.empty[stage], phase ^ 1u, abort_flag)) break;
+          uint8_t* st = s.ring[stage];
+          const uint32_t full = mapa_shared(smem_u32(&s.full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * (W_BYTES + mine * 128));
+          if (MODE == kSwiglu) {
+            tma_load_2d_pair(st, &tmW64, kb * 128, wrow, full);
+            tma_load_2d_pair(st + W_BYTES / 2, &tmW64, kb * 128, wrow + g.w_second, full);
+          } else {
+            tma_load_2d_pair(st, &tmW, kb * 128, wrow, full);
+          }
+          uint8_t* rows = st + W_BYTES;
+          if (mine == NT / 2) {
+            tma_load_2d_pair(rows, &tmA96, kb * 128, arow, full);
+          } else {
+            for (int i = 0; i < mine; i += 16) tma_load_2d_pair(rows + i * 128, &tmA16, kb * 128, arow + i, full);
+          }
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == kScaleProducer) {
+    // ---- TMA producer of the scales, counted on this CTA. A thread issues a copy every 150 to 200
+    // cycles, whatever its size: one thread for all seven of a stage took 600 us for 32768 rows ----
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int tile = cluster; tile < total && !*abort_flag; tile += nclusters) {
+        const Tile t = decode(s, g, tile, NT);
+        const int l0 = t.row0 - t.o_g;
+        const int sft = ((l0 & 127) + t.n + 127) / 128;      // scale tiles of all the rows
+        const int64_t wo = (int64_t)t.g * g.w_rows;
+        const int wl = t.n0 + (MODE == kSwiglu ? 64 : 128) * (int)rank;
+        const uint8_t* sw = scale_tile(g.w_scales, wo, t.g, min(wl, g.w_rows - 1), g.chunks);
+        const uint8_t* sw2 = scale_tile(g.w_scales, wo, t.g, wl + g.w_second, g.chunks);   // kSwiglu
+        const uint8_t* sa = scale_tile(g.a_scales, t.o_g, t.g, l0, g.chunks);
+        for (int kb = 0; kb < g.kstages; ++kb) {
+          if (!mbar_wait(&s.empty[stage], phase ^ 1u, abort_flag)) break;
+          uint8_t* sf = s.ring[stage] + W_BYTES + C::T_BYTES;
+          uint64_t* bar = &s.sland[stage];
+          const uint32_t sfb = 512u * (uint32_t)min(CPS, g.chunks - kb * CPS);
+          const size_t at = (size_t)kb * CPS * 512;
+          mbar_arrive_expect_tx(bar, sfb * ((MODE == kSwiglu ? 2 : 1) + sft));
+          bulk_load(sf, sw + at, sfb, bar);
+          if (MODE == kSwiglu) bulk_load(sf + C::SF_BYTES, sw2 + at, sfb, bar);
+          for (int i = 0; i < sft; ++i)
+            bulk_load(sf + (2 + i) * C::SF_BYTES, sa + (size_t)i * g.chunks * 512 + at, sfb, bar);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer (leader only) ------------------------------------------------------------
+    if (rank == 0 && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      int sl = 0;                // slot of scales
+      uint32_t sl_phase = 0;
+      bool ok = true;
+      for (int tile = cluster; ok && tile < total && !*abort_flag; tile += nclusters) {
+        const Tile t = decode(s, g, tile, NT);
+        const int npad = (t.n + 31) & ~31;
+        if (!mbar_wait(&s.tempty[acc], acc_phase ^ 1u, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * NT);
+        for (int kb = 0; kb < g.kstages; ++kb) {
+          if (!mbar_wait(&s.full[stage], phase, abort_flag) || !mbar_wait(&s.sfull[sl], sl_phase, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t w0 = smem_u32(s.ring[stage]);
+          const uint32_t rows = w0 + W_BYTES;
+          const uint32_t slot = tmem + C::SF_COL + (uint32_t)sl * C::SF_SLOT;
+          const int ksteps = min(CPS, g.chunks - kb * CPS) * (4 / CPS);      // K = 64 each
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k >= ksteps) break;
+            const uint32_t p = k / (4 / CPS);
+            umma_mx4_pair<NV>(d, sw128_kmajor_desc(w0 + k * 32), sw128_kmajor_desc(rows + k * 32),
+                              idesc_mx4<NV>(256, npad, NV ? 0u : 2u * (k & 1)), slot + 4 * p,
+                              slot + CPS * 4 + 6 * p, (kb > 0 || k > 0) ? 1u : 0u);
+          }
+          const uint32_t e_local = smem_u32(&s.empty[stage]);
+          umma_commit_pair(mapa_shared(e_local, 0));
+          umma_commit_pair(mapa_shared(e_local, 1));
+          if (++sl == C::SLOTS) {
+            sl = 0;
+            sl_phase ^= 1u;
+          }
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        const uint32_t f_local = smem_u32(&s.tfull[acc]);
+        umma_commit_pair(mapa_shared(f_local, 0));
+        umma_commit_pair(mapa_shared(f_local, 1));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+  } else if (warp >= 2 + kEpiWarps) {
+    // ---- scales of both CTAs: shared memory -> this warp's lane quarter of TMEM -----------------
+    const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+    int stage = 0;
+    uint32_t phase = 0;
+    int sl = 0;
+    // the stage SLOTS ago, whose MMAs read the slot last
+    int before = STAGES - C::SLOTS;
+    uint32_t before_phase = 1;   // the first waits return at once
+    bool ok = true;
+    for (int tile = cluster; ok && tile < total; tile += nclusters) {
+      const Tile t = decode(s, g, tile, NT);
+      // the rows start at the first or the third of their first scale tile's four columns
+      const int off = (t.row0 - t.o_g) & 127;
+      const bool two = off + t.n > 128;
+      // kSwiglu: the CTA's 64 channels are the first or the second half of their scale tile
+      const int upper = MODE == kSwiglu ? 8 * (int)rank : 0;
+      for (int kb = 0; kb < g.kstages; ++kb) {
+        // one lane waits, the warp follows it
+        int w_ok = 1;
+        if (lane == 0)
+          w_ok = mbar_wait(&s.sland[stage], phase, abort_flag) &&
+                 (C::SLOTS == STAGES || mbar_wait(&s.empty[before], before_phase, abort_flag));
+        w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
+        if (!w_ok) { ok = false; break; }
+        tc_fence_after();
+        const uint8_t* sf = s.ring[stage] + W_BYTES + C::T_BYTES;
+        const uint32_t slot = tmem + quarter + C::SF_COL + (uint32_t)sl * C::SF_SLOT;
+        // pieces past the row's end hold an earlier stage's scales: written, never used
+        if (MODE == kSwiglu) {
+          // columns 0, 1: 64 gate rows, 2, 3: the same up rows
+#pragma unroll
+          for (int p = 0; p < CPS; ++p) {
+            const uint2 a = *reinterpret_cast<const uint2*>(sf + p * 512 + lane * 16 + upper);
+            const uint2 b = *reinterpret_cast<const uint2*>(sf + C::SF_BYTES + p * 512 + lane * 16 + upper);
+            tmem_st_x4(slot + 4 * p, make_uint4(a.x, a.y, b.x, b.y));
+          }
+        } else {
+          tmem_st_scales<CPS>(slot, sf, lane);
+        }
+#pragma unroll
+        for (int p = 0; p < CPS; ++p) {
+          const uint8_t* piece = sf + 2 * C::SF_BYTES + p * 512 + lane * 16;
+          const uint4 a = *reinterpret_cast<const uint4*>(piece);
+          const uint4 b = two ? *reinterpret_cast<const uint4*>(piece + C::SF_BYTES) : make_uint4(0, 0, 0, 0);
+          const uint32_t col = slot + CPS * 4 + 6 * p;
+          tmem_st_x4(col, off ? make_uint4(a.z, a.w, b.x, b.y) : a);
+          tmem_st_x2(col + 4, off ? b.z : b.x, off ? b.w : b.y);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        // like the accumulators, TMEM columns are handed over by the tcgen05 fences
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.sfull[sl]), 0));
+        if (++sl == C::SLOTS) sl = 0;
+        if (++before == STAGES) {
+          before = 0;
+          before_phase ^= 1u;
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    // ---- epilogue (both CTAs): this CTA's 128 weight rows; the three warps of a quarter take
+    // turns over chunks of 16 columns -----------------------------------------------------------
+    const int q = warp & 3;
+    const int third = (warp - 2) >> 2;
+    float (*stg)[kStageLd] = reinterpret_cast<float (*)[kStageLd]>(s.turn + (warp - 2) * 8 * kStageLd);
+    float (*S)[kGroupLd] = reinterpret_cast<float (*)[kGroupLd]>(s.turn + third * 16 * kGroupLd);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    const float af = NV && g.a_factor ? *g.a_factor : 1.0f;
+    const float hf = NV && MODE == kSwiglu && g.h_factor ? *g.h_factor : 1.0f;
+    const float inv6 = 1.0f / (6.0f * hf);
+    for (int tile = cluster; tile < total; tile += nclusters) {
+      const Tile t = decode(s, g, tile, NT);
+      const float f = NV && g.w_factor ? af * g.w_factor[g.w_factor_per_group ? t.g : 0] : af;
+      int w_ok = 1;
+      if (lane == 0) w_ok = mbar_wait(&s.tfull[acc], acc_phase, abort_flag) ? 1 : 0;
+      w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
+      // all four warps of a range leave together: they meet at its barrier
+      if (MODE == kSwiglu) {
+        if (lane == 0) s.turn_ok[warp - 2] = w_ok;
+        range_bar(third);
+        w_ok = s.turn_ok[4 * third] & s.turn_ok[4 * third + 1] & s.turn_ok[4 * third + 2] & s.turn_ok[4 * third + 3];
+        range_bar(third);
+      }
+      if (!w_ok) break;
+      tc_fence_after();
+      const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * NT);
+#pragma unroll 1
+      for (int c = 16 * third; c < t.n; c += 16 * (kEpiWarps / 4)) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(base + c, v);
+        tmem_ld_wait();
+        if constexpr (MODE == kSwiglu) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) S[j][32 * q + lane] = __uint_as_float(v[j]);
+          range_bar(third);
+          epi_round_h_pair<NV>(g, t, c, t.n0 + 64 * (int)rank, q, lane, f, S, hf, inv6);
+          range_bar(third);                           // the rows may be written again
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(v[e + j]);
+            turn_around(x, stg, lane);
+            epi_store<MODE>(g, t, c + e, t.n0 + 128 * (int)rank + 32 * q + (lane & ~7), lane, f, x);
+            __syncwarp();
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.tempty[acc]), 0));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+
+  if (*abort_flag) {
+    set_status(g.status, MOE_ERR_TIMEOUT);
+    // let copies and MMAs already in flight land before the CTA's memory goes away
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();            // neither CTA leaves while the other may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
 // ---- host side -------------------------------------------------------------------------------
-template <int NT, int CPS, int MODE>
-int launch_as(const CUtensorMap& w, const CUtensorMap& a64, const CUtensorMap& a16, const Args& g,
-              int sm_count, cudaStream_t st) {
-  using C = Cfg<NT, CPS>;
-  constexpr size_t smem = sizeof(Storage<C::STAGES, C::STAGE>) + 1024;
-  static_assert(smem <= 227 * 1024 && C::STAGES >= 3, "shared memory budget");
-  auto kern = k_mx4_gemm<NT, CPS, MODE>;
+template <int CPS, int MODE>
+int launch_one(const moe_mx4_t& a, const moe_mx4_t& w, const Args& g, const DeviceInfo& dev, cudaStream_t st) {
+  constexpr size_t smem = sizeof(Storage<One<CPS>>) + 1024;
+  static_assert(smem <= 227 * 1024 && One<CPS>::STAGES >= 3, "shared memory budget");
+  CUtensorMap mw, a64, a16;
+  MOE_TRY(make_byte_map(&mw, w.codes, (uint64_t)w.rows, a.K / 2, 128));
+  MOE_TRY(make_byte_map(&a64, a.codes, (uint64_t)a.rows, a.K / 2, 64));
+  MOE_TRY(make_byte_map(&a16, a.codes, (uint64_t)a.rows, a.K / 2, 16));
+  auto kern = k_mx4_gemm<CPS, MODE>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return MOE_ERR_CUDA;
-  const cudaError_t e = launch_kernel(kern, sm_count, kThreads, smem, st, 1, w, a64, a16, g);
+  const cudaError_t e = launch_kernel(kern, dev.sm_count, kThreads, smem, st, 1, mw, a64, a16, g);
+  count_launch();
+  return cuda_rc(e);
+}
+
+template <int CPS, int MODE>
+int launch_pair(const moe_mx4_t& a, const moe_mx4_t& w, const Args& g, const DeviceInfo& dev, cudaStream_t st) {
+  constexpr size_t smem = sizeof(Storage<Pair<CPS>>) + 1024;
+  static_assert(smem <= 227 * 1024 && Pair<CPS>::STAGES >= 3, "shared memory budget");
+  CUtensorMap mw, w64, a96, a16;
+  MOE_TRY(make_byte_map(&mw, w.codes, (uint64_t)w.rows, a.K / 2, 128));
+  MOE_TRY(make_byte_map(&w64, w.codes, (uint64_t)w.rows, a.K / 2, 64));
+  MOE_TRY(make_byte_map(&a96, a.codes, (uint64_t)a.rows, a.K / 2, 96));
+  MOE_TRY(make_byte_map(&a16, a.codes, (uint64_t)a.rows, a.K / 2, 16));
+  auto kern = k_mx4_gemm_pair<CPS, MODE>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  // as many clusters as fit at once (cached per device), so that no CTA of the persistent tile
+  // loop waits for a cluster's place
+  static std::mutex mu;
+  static int clusters_of[64] = {0};
+  int n;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (clusters_of[dev.device] == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(dev.sm_count & ~1);
+      cfg.blockDim = dim3(kPairThreads);
+      cfg.dynamicSmemBytes = smem;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int fit = 0;
+      if (cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) != cudaSuccess || fit < 1) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+      }
+      clusters_of[dev.device] = min(fit, dev.sm_count / 2);
+    }
+    n = clusters_of[dev.device];
+  }
+  const cudaError_t e = launch_kernel(kern, 2 * n, kPairThreads, smem, st, 2, mw, w64, a96, a16, g);
   count_launch();
   return cuda_rc(e);
 }
@@ -591,19 +1061,14 @@ int launch_product(const moe_mx4_t& a, const moe_mx4_t& w, Args g, const DeviceI
   g.a_factor = a.factor;
   g.w_factor = w.factor;
   g.w_factor_per_group = w.factor_per_group;
-  CUtensorMap mw, a64, a16;
-  MOE_TRY(make_byte_map(&mw, w.codes, (uint64_t)w.rows, a.K / 2, 128));
-  MOE_TRY(make_byte_map(&a64, a.codes, (uint64_t)a.rows, a.K / 2, 64));
-  MOE_TRY(make_byte_map(&a16, a.codes, (uint64_t)a.rows, a.K / 2, 16));
-  // Few rows per group on average: a tile of 64 rows leaves room for more stages of weights in
-  // flight and a second accumulator. Else 192 rows, so that fewer tiles re-read the weights.
+  // Up to 64 rows per group on average (of the rows there may be): one CTA per tile.
   const bool few = a.rows <= 64ll * a.groups;
-#define MX4_LAUNCH(NT, CPS)                                                                        \
-  (swiglu             ? launch_as<NT, CPS, kSwiglu>(mw, a64, a16, g, dev.sm_count, st)            \
-   : g.mode == kStore ? launch_as<NT, CPS, kStore>(mw, a64, a16, g, dev.sm_count, st)             \
-                      : launch_as<NT, CPS, kFp32>(mw, a64, a16, g, dev.sm_count, st))
-  return is_nv(a) ? (few ? MX4_LAUNCH(64, 4) : MX4_LAUNCH(192, 4))
-               : (few ? MX4_LAUNCH(64, 2) : MX4_LAUNCH(192, 2));
+#define MX4_LAUNCH(KERNEL, CPS)                                              \
+  (swiglu             ? KERNEL<CPS, kSwiglu>(a, w, g, dev, st)               \
+   : g.mode == kStore ? KERNEL<CPS, kStore>(a, w, g, dev, st)                \
+                      : KERNEL<CPS, kFp32>(a, w, g, dev, st))
+  return is_nv(a) ? (few ? MX4_LAUNCH(launch_one, 4) : MX4_LAUNCH(launch_pair, 4))
+                  : (few ? MX4_LAUNCH(launch_one, 2) : MX4_LAUNCH(launch_pair, 2));
 #undef MX4_LAUNCH
 }
 
