@@ -253,6 +253,25 @@ __device__ __forceinline__ uint32_t idesc_mx4(int M, int N, uint32_t sf_id) {
          (static_cast<uint32_t>(M >> 7) << 27) | (sf_id << 4) | (sf_id << 29);
 }
 
+// The value of lane 0, which the compiler then knows to be the same in every lane.
+__device__ __forceinline__ int uni(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// mbar_wait by every lane of the warp, the same answer in each.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+
 // Untiled bulk copy global -> shared, completion counted on `bar`; 16-byte aligned both sides.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -397,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   auto& s = *reinterpret_cast<Storage<C>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uni(threadIdx.x >> 5), lane = threadIdx.x & 31;
   pdl_launch_dependents();
 
   if (threadIdx.x == 0) {
@@ -426,68 +445,74 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
-  const int total = s.toff[g.a.groups] * g.n_tiles;
+  const int total = uni(s.toff[g.a.groups] * g.n_tiles);
   volatile int* abort_flag = &s.abort_flag;
 
+  // The producer and the issuer run as whole warps in step, on values that the compiler knows to be
+  // uniform, and one lane issues: TMA, MMA and commit take their operands from uniform registers.
   if (warp == 0) {
     // ---- TMA producer --------------------------------------------------------------------
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int tile = blockIdx.x; tile < total && !*abort_flag; tile += gridDim.x) {
-        const Tile t = decode(s, g, tile, NT);
-        const int big = t.n / 64, small = (t.n % 64 + 15) / 16;
-        const int wrow = t.g * g.w_rows + t.n0;
-        const int64_t wo = (int64_t)t.g * g.w_rows;
-        const uint8_t* sw = scale_tile(g.w_scales, wo, t.g, t.n0, g.chunks);
-        const uint8_t* sw2 = scale_tile(g.w_scales, wo, t.g, t.n0 + g.w_second, g.chunks);
-        const uint8_t* sa = scale_tile(g.a_scales, t.o_g, t.g, t.row0 - t.o_g, g.chunks);
-        for (int kb = 0; kb < g.kstages; ++kb) {
-          if (!mbar_wait(&s.empty[stage], phase ^ 1u, abort_flag)) break;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      const Tile t = decode(s, g, tile, NT);
+      const int n = uni(t.n), grp = uni(t.g), n0 = uni(t.n0), row0 = uni(t.row0), o_g = uni(t.o_g);
+      const bool two = uni(t.blocks) == 2;
+      const int small = n < NT ? (n + 15) / 16 : 0;          // boxes of 16 rows, or one of 64
+      const int wrow = grp * g.w_rows + n0;
+      const int64_t wo = (int64_t)grp * g.w_rows;
+      const uint8_t* sw = scale_tile(g.w_scales, wo, grp, n0, g.chunks);
+      const uint8_t* sw2 = scale_tile(g.w_scales, wo, grp, n0 + g.w_second, g.chunks);
+      const uint8_t* sa = scale_tile(g.a_scales, o_g, grp, row0 - o_g, g.chunks);
+      for (int kb = 0; kb < g.kstages; ++kb) {
+        ok = warp_wait(&s.empty[stage], phase ^ 1u, abort_flag);
+        if (!ok) break;
+        if (elect_one()) {
           uint8_t* st = s.ring[stage];
           uint64_t* bar = &s.full[stage];
           const uint32_t sfb = 512u * (uint32_t)min(CPS, g.chunks - kb * CPS);
-          mbar_arrive_expect_tx(bar, t.blocks * (W_BYTES + sfb) + (big * 64 + small * 16) * 128 + sfb);
+          mbar_arrive_expect_tx(bar, (two ? 2 : 1) * (W_BYTES + sfb) + (small ? small * 16 : NT) * 128 + sfb);
           tma_load_2d(st, &tmW, kb * 128, wrow, bar);
-          if (t.blocks == 2) tma_load_2d(st + W_BYTES, &tmW, kb * 128, wrow + g.w_second, bar);
+          if (two) tma_load_2d(st + W_BYTES, &tmW, kb * 128, wrow + g.w_second, bar);
           uint8_t* rows = st + 2 * W_BYTES;
-          if (big) tma_load_2d(rows, &tmA64, kb * 128, t.row0, bar);
-          for (int i = 0; i < small; ++i)
-            tma_load_2d(rows + (big * 64 + i * 16) * 128, &tmA16, kb * 128, t.row0 + big * 64 + i * 16, bar);
+          if (!small) tma_load_2d(rows, &tmA64, kb * 128, row0, bar);
+          for (int i = 0; i < small; ++i) tma_load_2d(rows + i * 16 * 128, &tmA16, kb * 128, row0 + i * 16, bar);
           uint8_t* sf = rows + C::T_BYTES;
           const size_t at = (size_t)kb * CPS * 512;
           bulk_load(sf, sw + at, sfb, bar);
-          if (t.blocks == 2) bulk_load(sf + C::SF_BYTES, sw2 + at, sfb, bar);
+          if (two) bulk_load(sf + C::SF_BYTES, sw2 + at, sfb, bar);
           bulk_load(sf + 2 * C::SF_BYTES, sa + at, sfb, bar);     // 64 rows lie in one scale tile
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
   } else if (warp == 1) {
     // ---- MMA issuer --------------------------------------------------------------------------
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      int sl = 0;                // slot of scales
-      uint32_t sl_phase = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total && !*abort_flag; tile += gridDim.x) {
-        const Tile t = decode(s, g, tile, NT);
-        const int npad = (t.n + 15) & ~15;
-        if (!mbar_wait(&s.tempty[acc], acc_phase ^ 1u, abort_flag)) break;
+    int stage = 0;
+    uint32_t phase = 0;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    int sl = 0;                // slot of scales
+    uint32_t sl_phase = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      const Tile t = decode(s, g, tile, NT);
+      const int npad = (uni(t.n) + 15) & ~15;
+      const bool two = uni(t.blocks) == 2;
+      ok = warp_wait(&s.tempty[acc], acc_phase ^ 1u, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)(acc * 2 * NT);
+      for (int kb = 0; kb < g.kstages; ++kb) {
+        ok = warp_wait(&s.full[stage], phase, abort_flag) && warp_wait(&s.sfull[sl], sl_phase, abort_flag);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(acc * 2 * NT);
-        for (int kb = 0; kb < g.kstages; ++kb) {
-          if (!mbar_wait(&s.full[stage], phase, abort_flag) || !mbar_wait(&s.sfull[sl], sl_phase, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        if (elect_one()) {
           const uint32_t w0 = smem_u32(s.ring[stage]);
           const uint32_t rows = w0 + 2 * W_BYTES;
           const uint32_t slot = tmem + C::SF_COL + (uint32_t)sl * C::SF_SLOT;
@@ -501,25 +526,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t sfb = slot + CPS * 8 + 2 * p;
             const uint32_t go = (kb > 0 || k > 0) ? 1u : 0u;
             umma_mx4<NV>(d, sw128_kmajor_desc(w0 + k * 32), db, idesc, slot + 4 * p, sfb, go);
-            if (t.blocks == 2)
+            if (two)
               umma_mx4<NV>(d + NT, sw128_kmajor_desc(w0 + W_BYTES + k * 32), db, idesc, slot + CPS * 4 + 4 * p,
                            sfb, go);
           }
           umma_commit(&s.empty[stage]);
-          if (++sl == C::SLOTS) {
-            sl = 0;
-            sl_phase ^= 1u;
-          }
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (!ok) break;
-        umma_commit(&s.tfull[acc]);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
+        __syncwarp();
+        if (++sl == C::SLOTS) {
+          sl = 0;
+          sl_phase ^= 1u;
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
+      if (!ok) break;
+      if (elect_one()) umma_commit(&s.tfull[acc]);
+      __syncwarp();
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
     }
   } else if (warp >= 2 + kEpiWarps) {
     // ---- scales: shared memory -> this warp's lane quarter of TMEM ----------------------------
@@ -684,7 +711,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   auto& s = *reinterpret_cast<Storage<C>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uni(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();            // 0: leader, 1: peer
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
   pdl_launch_dependents();
@@ -719,23 +746,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
-  const int total = s.toff[g.a.groups] * g.n_tiles;
+  const int total = uni(s.toff[g.a.groups] * g.n_tiles);
   volatile int* abort_flag = &s.abort_flag;
 
+  // whole warps in step with one lane issuing, as in k_mx4_gemm
   if (warp == 0) {
     // ---- TMA producer of the operands (both CTAs), counted on the leader -----------------------
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int tile = cluster; tile < total && !*abort_flag; tile += nclusters) {
-        const Tile t = decode(s, g, tile, NT);
-        const int mine = ((t.n + 31) & ~31) / 2;             // rows of this CTA's half
-        const int arow = t.row0 + mine * (int)rank;
-        // this CTA's first weight row; past the group's end (an odd number of 128-row blocks)
-        // the boxes read on or are zeros: those channels are dropped
-        const int wrow = t.g * g.w_rows + t.n0 + (MODE == kSwiglu ? 64 : 128) * (int)rank;
-        for (int kb = 0; kb < g.kstages; ++kb) {
-          if (!mbar_wait(&s.empty[stage], phase ^ 1u, abort_flag)) break;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = cluster; ok && tile < total; tile += nclusters) {
+      const Tile t = decode(s, g, tile, NT);
+      const int mine = ((uni(t.n) + 31) & ~31) / 2;          // rows of this CTA's half
+      const int arow = uni(t.row0) + mine * (int)rank;
+      // this CTA's first weight row; past the group's end (an odd number of 128-row blocks)
+      // the boxes read on or are zeros: those channels are dropped
+      const int wrow = uni(t.g) * g.w_rows + uni(t.n0) + (MODE == kSwiglu ? 64 : 128) * (int)rank;
+      for (int kb = 0; kb < g.kstages; ++kb) {
+        ok = warp_wait(&s.empty[stage], phase ^ 1u, abort_flag);
+        if (!ok) break;
+        if (elect_one()) {
           uint8_t* st = s.ring[stage];
           const uint32_t full = mapa_shared(smem_u32(&s.full[stage]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * (W_BYTES + mine * 128));
@@ -751,30 +781,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           } else {
             for (int i = 0; i < mine; i += 16) tma_load_2d_pair(rows + i * 128, &tmA16, kb * 128, arow + i, full);
           }
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
   } else if (warp == kScaleProducer) {
     // ---- TMA producer of the scales, counted on this CTA. A thread issues a copy every 150 to 200
     // cycles, whatever its size: one thread for all seven of a stage took 600 us for 32768 rows ----
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int tile = cluster; tile < total && !*abort_flag; tile += nclusters) {
-        const Tile t = decode(s, g, tile, NT);
-        const int l0 = t.row0 - t.o_g;
-        const int sft = ((l0 & 127) + t.n + 127) / 128;      // scale tiles of all the rows
-        const int64_t wo = (int64_t)t.g * g.w_rows;
-        const int wl = t.n0 + (MODE == kSwiglu ? 64 : 128) * (int)rank;
-        const uint8_t* sw = scale_tile(g.w_scales, wo, t.g, min(wl, g.w_rows - 1), g.chunks);
-        const uint8_t* sw2 = scale_tile(g.w_scales, wo, t.g, wl + g.w_second, g.chunks);   // kSwiglu
-        const uint8_t* sa = scale_tile(g.a_scales, t.o_g, t.g, l0, g.chunks);
-        for (int kb = 0; kb < g.kstages; ++kb) {
-          if (!mbar_wait(&s.empty[stage], phase ^ 1u, abort_flag)) break;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = cluster; ok && tile < total; tile += nclusters) {
+      const Tile t = decode(s, g, tile, NT);
+      const int grp = uni(t.g), o_g = uni(t.o_g), l0 = uni(t.row0) - o_g;
+      const int sft = ((l0 & 127) + uni(t.n) + 127) / 128;   // scale tiles of all the rows
+      const int64_t wo = (int64_t)grp * g.w_rows;
+      const int wl = uni(t.n0) + (MODE == kSwiglu ? 64 : 128) * (int)rank;
+      const uint8_t* sw = scale_tile(g.w_scales, wo, grp, min(wl, g.w_rows - 1), g.chunks);
+      const uint8_t* sw2 = scale_tile(g.w_scales, wo, grp, wl + g.w_second, g.chunks);     // kSwiglu
+      const uint8_t* sa = scale_tile(g.a_scales, o_g, grp, l0, g.chunks);
+      for (int kb = 0; kb < g.kstages; ++kb) {
+        ok = warp_wait(&s.empty[stage], phase ^ 1u, abort_flag);
+        if (!ok) break;
+        if (elect_one()) {
           uint8_t* sf = s.ring[stage] + W_BYTES + C::T_BYTES;
           uint64_t* bar = &s.sland[stage];
           const uint32_t sfb = 512u * (uint32_t)min(CPS, g.chunks - kb * CPS);
@@ -784,35 +817,35 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (MODE == kSwiglu) bulk_load(sf + C::SF_BYTES, sw2 + at, sfb, bar);
           for (int i = 0; i < sft; ++i)
             bulk_load(sf + (2 + i) * C::SF_BYTES, sa + (size_t)i * g.chunks * 512 + at, sfb, bar);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
   } else if (warp == 1) {
     // ---- MMA issuer (leader only) ------------------------------------------------------------
-    if (rank == 0 && lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      int sl = 0;                // slot of scales
-      uint32_t sl_phase = 0;
-      bool ok = true;
-      for (int tile = cluster; ok && tile < total && !*abort_flag; tile += nclusters) {
-        const Tile t = decode(s, g, tile, NT);
-        const int npad = (t.n + 31) & ~31;
-        if (!mbar_wait(&s.tempty[acc], acc_phase ^ 1u, abort_flag)) break;
+    int stage = 0;
+    uint32_t phase = 0;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    int sl = 0;                // slot of scales
+    uint32_t sl_phase = 0;
+    bool ok = rank == 0;
+    for (int tile = cluster; ok && tile < total; tile += nclusters) {
+      const Tile t = decode(s, g, tile, NT);
+      const int npad = (uni(t.n) + 31) & ~31;
+      ok = warp_wait(&s.tempty[acc], acc_phase ^ 1u, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)(acc * NT);
+      for (int kb = 0; kb < g.kstages; ++kb) {
+        ok = warp_wait(&s.full[stage], phase, abort_flag) && warp_wait(&s.sfull[sl], sl_phase, abort_flag);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(acc * NT);
-        for (int kb = 0; kb < g.kstages; ++kb) {
-          if (!mbar_wait(&s.full[stage], phase, abort_flag) || !mbar_wait(&s.sfull[sl], sl_phase, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+        if (elect_one()) {
           const uint32_t w0 = smem_u32(s.ring[stage]);
           const uint32_t rows = w0 + W_BYTES;
           const uint32_t slot = tmem + C::SF_COL + (uint32_t)sl * C::SF_SLOT;
@@ -828,22 +861,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           const uint32_t e_local = smem_u32(&s.empty[stage]);
           umma_commit_pair(mapa_shared(e_local, 0));
           umma_commit_pair(mapa_shared(e_local, 1));
-          if (++sl == C::SLOTS) {
-            sl = 0;
-            sl_phase ^= 1u;
-          }
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (!ok) break;
+        __syncwarp();
+        if (++sl == C::SLOTS) {
+          sl = 0;
+          sl_phase ^= 1u;
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) {
         const uint32_t f_local = smem_u32(&s.tfull[acc]);
         umma_commit_pair(mapa_shared(f_local, 0));
         umma_commit_pair(mapa_shared(f_local, 1));
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
       }
+      __syncwarp();
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
     }
   } else if (warp >= 2 + kEpiWarps) {
     // ---- scales of both CTAs: shared memory -> this warp's lane quarter of TMEM -----------------
