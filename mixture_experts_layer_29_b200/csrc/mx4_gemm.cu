@@ -68,9 +68,9 @@ constexpr uint32_t kTmemCols = 512;
 // neither the writes (a row at a time) nor the reads (16 bytes of 8 rows) meet in a bank
 constexpr int kStageLd = 36;
 constexpr int kGroupLd = 132;
-constexpr int kEpiFloats = kEpiWarps / 4 * 16 * kGroupLd;
+constexpr int kEpiFloats = kEpiWarps * 8 * kStageLd;
 constexpr int kEpiBytes = kEpiFloats * 4;
-static_assert(kEpiFloats >= kEpiWarps * 8 * kStageLd, "staging rows");
+static_assert(kEpiFloats >= kEpiWarps / 4 * 8 * kGroupLd, "staging rows");
 constexpr int W_BYTES = 128 * 128;                  // a weight block's stage: 128 rows x 128 bytes
 
 // kStore: y in bf16; kFp32: y in fp32, stored or added to the tokens' sums; kSwiglu: h in 4 bits
@@ -141,8 +141,8 @@ struct alignas(1024) Storage {
   int abort_flag;
   int offs[kMx4MaxGroups + 1];
   int toff[kMx4MaxGroups + 1];
-  int turn_ok[kEpiWarps];     // the warps of a channel range tell each other whether to go on
-  // staging rows of the epilogue: [warp][8][kStageLd], or [four warps][16][kGroupLd] where the
+  int turn_ok[kEpiWarps];     // the warps of a column range tell each other whether to go on
+  // staging rows of the epilogue: [warp][8][kStageLd], or [four warps][8][kGroupLd] where the
   // warps of a channel range work together
   alignas(16) float turn[kEpiFloats];
 };
@@ -242,6 +242,16 @@ __device__ __forceinline__ void umma_mx4_pair(uint32_t d, uint64_t a, uint64_t b
         "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
   }
+}
+
+// Arrive on the mbarrier at `bar` (this CTA's shared memory) and on the one at the same place in the
+// pair's other CTA once the tcgen05.mma issued so far have completed.
+__device__ __forceinline__ void umma_commit_both(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
 }
 
 // Instruction descriptor, block-scaled 4-bit kinds: A and B e2m1 (bits 7-9 and 10-11 = 1), both
@@ -662,43 +672,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- CTA pairs ---------------------------------------------------------------------------------
 // h of the pair kernel, where lanes 0-63 hold the gate and 64-127 the up rows of the CTA's 64
-// channels: the four warps of a channel range (one per lane quarter) have staged 16 rows from c on
-// as S[row][TMEM lane]; this warp takes rows 4 q to 4 q + 3, two at a time, 4 channels per lane.
-// ch: the CTA's first channel.
+// channels: the four warps of a column range (one per lane quarter) have staged 8 rows from c on as
+// S[row][TMEM lane]; this warp takes rows 2 q and 2 q + 1, 4 channels per lane. ch: the CTA's first
+// channel.
 template <bool NV>
 __device__ __forceinline__ void epi_round_h_pair(const Args& a, const Tile& t, int c, int ch, int q, int lane, float f,
                                                  const float (*S)[kGroupLd], float hf, float inv6) {
+  const int r = 2 * q + (lane >> 4), k = 4 * (lane & 15);
+  const float4 G = *reinterpret_cast<const float4*>(&S[r][k]);
+  const float4 U = *reinterpret_cast<const float4*>(&S[r][64 + k]);
+  const float gv[4] = {G.x, G.y, G.z, G.w}, uv[4] = {U.x, U.y, U.z, U.w};
+  float h[4];
+  uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < 4; e += 2) {
-    const int r = 4 * q + e + (lane >> 4), k = 4 * (lane & 15);
-    const float4 G = *reinterpret_cast<const float4*>(&S[r][k]);
-    const float4 U = *reinterpret_cast<const float4*>(&S[r][64 + k]);
-    const float gv[4] = {G.x, G.y, G.z, G.w}, uv[4] = {U.x, U.y, U.z, U.w};
-    float h[4];
-    uint32_t top = 0;
+  for (int i = 0; i < 4; ++i) {
+    const float x = gv[i] * f;
+    h[i] = __fdividef(x, 1.0f + __expf(-x)) * (uv[i] * f);
+    top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = gv[i] * f;
-      h[i] = __fdividef(x, 1.0f + __expf(-x)) * (uv[i] * f);
-      top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
-    }
-#pragma unroll
-    for (int o = 1; o < mx4_block(NV) / 4; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float by;
-    const uint32_t byte = round_scale<NV>(top, hf, inv6, by);
-    const uint32_t v = e2m1x2(scaled_h(h[0], by), scaled_h(h[1], by)) | e2m1x2(scaled_h(h[2], by), scaled_h(h[3], by)) << 8;
-    if (c + r < t.n) {
-      const int row = t.row0 + c + r;
-      *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.out) + (size_t)row * (a.n_out / 2) + (ch + k) / 2) = (uint16_t)v;
-      if (k % mx4_block(NV) == 0)
-        a.h_scales[mx4_scale_at(t.o_g, t.g, row - t.o_g, (ch + k) / mx4_block(NV), a.n_out / (4 * mx4_block(NV)))] =
-            (uint8_t)byte;
-    }
-    __syncwarp();
+  for (int o = 1; o < mx4_block(NV) / 4; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float by;
+  const uint32_t byte = round_scale<NV>(top, hf, inv6, by);
+  const uint32_t v = e2m1x2(scaled_h(h[0], by), scaled_h(h[1], by)) | e2m1x2(scaled_h(h[2], by), scaled_h(h[3], by)) << 8;
+  if (c + r < t.n) {
+    const int row = t.row0 + c + r;
+    *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.out) + (size_t)row * (a.n_out / 2) + (ch + k) / 2) = (uint16_t)v;
+    if (k % mx4_block(NV) == 0)
+      a.h_scales[mx4_scale_at(t.o_g, t.g, row - t.o_g, (ch + k) / mx4_block(NV), a.n_out / (4 * mx4_block(NV)))] =
+          (uint8_t)byte;
   }
 }
 
-// The epilogue warps of one channel range (four warps) meet here; named barriers 1 to 3.
+// The epilogue warps of one column range (four warps) meet here; named barriers 1 to 3.
 __device__ __forceinline__ void range_bar(int third) { asm volatile("bar.sync %0, 128;" ::"r"(third + 1) : "memory"); }
 
 template <int CPS, int MODE>
@@ -858,9 +864,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                               idesc_mx4<NV>(256, npad, NV ? 0u : 2u * (k & 1)), slot + 4 * p,
                               slot + CPS * 4 + 6 * p, (kb > 0 || k > 0) ? 1u : 0u);
           }
-          const uint32_t e_local = smem_u32(&s.empty[stage]);
-          umma_commit_pair(mapa_shared(e_local, 0));
-          umma_commit_pair(mapa_shared(e_local, 1));
+          umma_commit_both(&s.empty[stage]);
         }
         __syncwarp();
         if (++sl == C::SLOTS) {
@@ -873,11 +877,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       }
       if (!ok) break;
-      if (elect_one()) {
-        const uint32_t f_local = smem_u32(&s.tfull[acc]);
-        umma_commit_pair(mapa_shared(f_local, 0));
-        umma_commit_pair(mapa_shared(f_local, 1));
-      }
+      if (elect_one()) umma_commit_both(&s.tfull[acc]);
       __syncwarp();
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
@@ -953,7 +953,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3;
     const int third = (warp - 2) >> 2;
     float (*stg)[kStageLd] = reinterpret_cast<float (*)[kStageLd]>(s.turn + (warp - 2) * 8 * kStageLd);
-    float (*S)[kGroupLd] = reinterpret_cast<float (*)[kGroupLd]>(s.turn + third * 16 * kGroupLd);
+    float (*S)[kGroupLd] = reinterpret_cast<float (*)[kGroupLd]>(s.turn + third * 8 * kGroupLd);
     int acc = 0;
     uint32_t acc_phase = 0;
     const float af = NV && g.a_factor ? *g.a_factor : 1.0f;
@@ -982,10 +982,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tmem_ld_wait();
         if constexpr (MODE == kSwiglu) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) S[j][32 * q + lane] = __uint_as_float(v[j]);
-          range_bar(third);
-          epi_round_h_pair<NV>(g, t, c, t.n0 + 64 * (int)rank, q, lane, f, S, hf, inv6);
-          range_bar(third);                           // the rows may be written again
+          for (int e = 0; e < 16; e += 8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) S[j][32 * q + lane] = __uint_as_float(v[e + j]);
+            range_bar(third);
+            epi_round_h_pair<NV>(g, t, c + e, t.n0 + 64 * (int)rank, q, lane, f, S, hf, inv6);
+            range_bar(third);                         // the rows may be written again
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 16; e += 8) {
