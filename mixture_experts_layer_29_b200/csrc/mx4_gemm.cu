@@ -23,11 +23,11 @@
 // Warps:
 //   0           TMA producer: per stage of K = 256 elements (128 bytes, 128-byte swizzle) the
 //               weight boxes, the tile's rows in a few boxes, and (in the pair kernel a warp of
-//               its own, 18) the block scales as plain bulk copies of the 512-byte pieces
+//               its own, 22) the block scales as plain bulk copies of the 512-byte pieces
 //   1           TMEM owner and MMA issuer (the pair's leader): 4 tcgen05.mma of K = 64 per stage
 //               and weight block
 //   2-13        epilogue: tcgen05.ld, math, global stores
-//   14-17       scales: each warp copies the stage's pieces from shared memory to its lane quarter
+//   14-17       scales (pair: 14-21, four warps for every other stage): each warp copies the stage's pieces from shared memory to its lane quarter
 //               of TMEM with tcgen05.st (the MMA reads them in all four quarters)
 // The scales of the stages take turns over the TMEM columns that are left, 3 to 5 slots: with fewer
 // slots than stages the scale warps wait, before they overwrite a slot, until the MMAs that read it
@@ -61,8 +61,8 @@ namespace {
 constexpr int kEpiWarps = 12;                       // three per TMEM lane quarter
 constexpr int kScaleWarps = 4;
 constexpr int kThreads = 64 + (kEpiWarps + kScaleWarps) * 32;
-constexpr int kScaleProducer = 2 + kEpiWarps + kScaleWarps;    // pair kernel: a warp more
-constexpr int kPairThreads = kThreads + 32;
+constexpr int kScaleProducer = 2 + kEpiWarps + 2 * kScaleWarps;    // pair kernel: 8 scale warps, and one more
+constexpr int kPairThreads = (kScaleProducer + 1) * 32;
 constexpr uint32_t kTmemCols = 512;
 // a warp's staging rows: 8 rows of 32 channels, 4 floats apart from a multiple of 32, so that
 // neither the writes (a row at a time) nor the reads (16 bytes of 8 rows) meet in a bank
@@ -107,6 +107,7 @@ struct One {
   static constexpr int SF_BYTES = CPS * 512;               // a stage's pieces of 128 rows
   static constexpr int STAGE = 2 * W_BYTES + T_BYTES + 3 * SF_BYTES;   // two weight blocks, the rows
   static constexpr int STAGES = (227 * 1024 - 12 * 1024 - kEpiBytes) / STAGE;
+  static constexpr int SF_STAGE = 16, SF_STAGES = 1;       // no ring of scales: they come with the operands
   static constexpr int SF_COL = 4 * NT;                    // after two accumulators of two blocks
   static constexpr int SF_SLOT = CPS * 10;                 // W0: CPS x 4, W1: CPS x 4, rows: CPS x 2
   static constexpr int SLOTS = STAGES;
@@ -118,25 +119,31 @@ struct Pair {
   static constexpr int NT = 192;
   static constexpr int T_BYTES = NT / 2 * 128;             // this CTA's half of the rows
   static constexpr int SF_BYTES = CPS * 512;
-  static constexpr int STAGE = W_BYTES + T_BYTES + 4 * SF_BYTES;       // gate and up (or W), the rows: two
-  static constexpr int STAGES = (227 * 1024 - 12 * 1024 - kEpiBytes) / STAGE;
+  static constexpr int STAGE = W_BYTES + T_BYTES;
+  static constexpr int STAGES = 6;
+  static constexpr int SF_STAGE = 4 * SF_BYTES;            // gate and up (or W), the rows: two scale tiles
+  static constexpr int SF_STAGES = CPS == 4 ? 4 : 6;       // of a ring of their own
   static constexpr int SF_COL = 2 * NT;                    // after two accumulators
   static constexpr int SF_SLOT = CPS * 10;                 // W: CPS x 4, rows: CPS x 6
   static constexpr int FIT = ((int)kTmemCols - SF_COL) / SF_SLOT;
   static constexpr int SLOTS = FIT < STAGES ? FIT : STAGES;
   static_assert(STAGE % 1024 == 0, "128-byte-swizzled boxes need 1024-byte alignment");
   static_assert(SLOTS >= 3, "TMEM budget");
+  static_assert(STAGES % 2 == 0 && SF_STAGES % 2 == 0, "the two sets of scale warps keep their own stages");
 };
 
 template <class C>
 struct alignas(1024) Storage {
   uint8_t ring[C::STAGES][C::STAGE];
-  uint64_t full[C::STAGES];   // operands (pair: of both CTAs, on the leader) have landed
-  uint64_t sland[C::STAGES];  // pair: this CTA's scales have landed
+  alignas(16) uint8_t sring[C::SF_STAGES][C::SF_STAGE];
+  uint64_t full[C::STAGES];   // operands have landed; pair, on the leader: those of both CTAs, and the
+                              // scales of both CTAs are in TMEM
   uint64_t empty[C::STAGES];
+  uint64_t sland[C::SF_STAGES];    // pair: this CTA's scales have landed, and have been read
+  uint64_t sempty[C::SF_STAGES];
   uint64_t tfull[2];
   uint64_t tempty[2];
-  uint64_t sfull[C::SLOTS];   // a slot of scales is in TMEM (pair: of both CTAs, on the leader)
+  uint64_t sfull[C::SLOTS];   // one CTA: a slot of scales is in TMEM
   uint32_t tmem_base;
   int abort_flag;
   int offs[kMx4MaxGroups + 1];
@@ -280,6 +287,19 @@ __device__ __forceinline__ bool elect_one() {
 // mbar_wait by every lane of the warp, the same answer in each.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+
+// Whether the phase of the given parity is over, without waiting for it.
+__device__ __forceinline__ uint32_t mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok;
 }
 
 // Untiled bulk copy global -> shared, completion counted on `bar`; 16-byte aligned both sides.
@@ -724,15 +744,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&s.full[i], 1);
-      mbar_init(&s.sland[i], 1);
+      mbar_init(&s.full[i], 1 + 2 * kScaleWarps);
       mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < C::SF_STAGES; ++i) {
+      mbar_init(&s.sland[i], 1);
+      mbar_init(&s.sempty[i], kScaleWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.tfull[i], 1);
       mbar_init(&s.tempty[i], 2 * kEpiWarps);
     }
-    for (int i = 0; i < C::SLOTS; ++i) mbar_init(&s.sfull[i], 2 * kScaleWarps);
     s.abort_flag = 0;
     fence_barrier_init();
     prefetch_tensormap(MODE == kSwiglu ? &tmW64 : &tmW);
@@ -796,8 +818,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     }
   } else if (warp == kScaleProducer) {
-    // ---- TMA producer of the scales, counted on this CTA. A thread issues a copy every 150 to 200
-    // cycles, whatever its size: one thread for all seven of a stage took 600 us for 32768 rows ----
+    // ---- TMA producer of the scales, counted on this CTA, into a ring that the scale warps free
+    // as soon as they have read a stage ----------------------------------------------------------
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -811,10 +833,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const uint8_t* sw2 = scale_tile(g.w_scales, wo, grp, wl + g.w_second, g.chunks);     // kSwiglu
       const uint8_t* sa = scale_tile(g.a_scales, o_g, grp, l0, g.chunks);
       for (int kb = 0; kb < g.kstages; ++kb) {
-        ok = warp_wait(&s.empty[stage], phase ^ 1u, abort_flag);
+        ok = warp_wait(&s.sempty[stage], phase ^ 1u, abort_flag);
         if (!ok) break;
         if (elect_one()) {
-          uint8_t* sf = s.ring[stage] + W_BYTES + C::T_BYTES;
+          uint8_t* sf = s.sring[stage];
           uint64_t* bar = &s.sland[stage];
           const uint32_t sfb = 512u * (uint32_t)min(CPS, g.chunks - kb * CPS);
           const size_t at = (size_t)kb * CPS * 512;
@@ -825,7 +847,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             bulk_load(sf + (2 + i) * C::SF_BYTES, sa + (size_t)i * g.chunks * 512 + at, sfb, bar);
         }
         __syncwarp();
-        if (++stage == STAGES) {
+        if (++stage == C::SF_STAGES) {
           stage = 0;
           phase ^= 1u;
         }
@@ -838,7 +860,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     int sl = 0;                // slot of scales
-    uint32_t sl_phase = 0;
+    uint32_t ready = 0;        // the coming stage was seen to be full
     bool ok = rank == 0;
     for (int tile = cluster; ok && tile < total; tile += nclusters) {
       const Tile t = decode(s, g, tile, NT);
@@ -848,9 +870,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       tc_fence_after();
       const uint32_t d = tmem + (uint32_t)(acc * NT);
       for (int kb = 0; kb < g.kstages; ++kb) {
-        ok = warp_wait(&s.full[stage], phase, abort_flag) && warp_wait(&s.sfull[sl], sl_phase, abort_flag);
+        if (!__all_sync(0xffffffffu, ready)) ok = warp_wait(&s.full[stage], phase, abort_flag);
         if (!ok) break;
         tc_fence_after();
+        // look at the next stage's barrier before this stage's MMAs: the answer takes a while
+        const int next = stage + 1 == STAGES ? 0 : stage + 1;
+        ready = mbar_test(&s.full[next], next ? phase : phase ^ 1u);
         if (elect_one()) {
           const uint32_t w0 = smem_u32(s.ring[stage]);
           const uint32_t rows = w0 + W_BYTES;
@@ -867,14 +892,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           umma_commit_both(&s.empty[stage]);
         }
         __syncwarp();
-        if (++sl == C::SLOTS) {
-          sl = 0;
-          sl_phase ^= 1u;
-        }
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        if (++sl == C::SLOTS) sl = 0;
+        stage = next;
+        if (next == 0) phase ^= 1u;
       }
       if (!ok) break;
       if (elect_one()) umma_commit_both(&s.tfull[acc]);
@@ -883,13 +903,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (acc == 0) acc_phase ^= 1u;
     }
   } else if (warp >= 2 + kEpiWarps) {
-    // ---- scales of both CTAs: shared memory -> this warp's lane quarter of TMEM -----------------
+    // ---- scales of both CTAs: shared memory -> this warp's lane quarter of TMEM. A stage takes a
+    // warp some 560 cycles, longer than its MMAs: two sets of four warps take turns ---------------
     const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
-    int stage = 0;
+    const int set = (warp - 2 - kEpiWarps) / kScaleWarps;
+    int turn = 0;                // of the set whose stage it is
+    int stage = set;             // this set's next one, of the scales' ring,
     uint32_t phase = 0;
-    int sl = 0;
+    int ostage = set;            // of the operands' ring,
+    int sl = set;                // and its slot
     // the stage SLOTS ago, whose MMAs read the slot last
-    int before = STAGES - C::SLOTS;
+    int before = STAGES - C::SLOTS + set;
     uint32_t before_phase = 1;   // the first waits return at once
     bool ok = true;
     for (int tile = cluster; ok && tile < total; tile += nclusters) {
@@ -900,49 +924,64 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       // kSwiglu: the CTA's 64 channels are the first or the second half of their scale tile
       const int upper = MODE == kSwiglu ? 8 * (int)rank : 0;
       for (int kb = 0; kb < g.kstages; ++kb) {
+        turn ^= 1;
+        if ((turn ^ 1) != set) continue;
         // one lane waits, the warp follows it
         int w_ok = 1;
-        if (lane == 0)
-          w_ok = mbar_wait(&s.sland[stage], phase, abort_flag) &&
-                 (C::SLOTS == STAGES || mbar_wait(&s.empty[before], before_phase, abort_flag));
+        if (lane == 0) w_ok = mbar_wait(&s.sland[stage], phase, abort_flag) ? 1 : 0;
+        w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
+        if (!w_ok) { ok = false; break; }
+        // pieces past the row's end hold an earlier stage's scales: written, never used
+        const uint8_t* sf = s.sring[stage] + lane * 16;
+        uint4 w[CPS], r[CPS];
+        uint2 r2[CPS];
+#pragma unroll
+        for (int p = 0; p < CPS; ++p) {
+          if (MODE == kSwiglu) {
+            // columns 0, 1: 64 gate rows, 2, 3: the same up rows
+            const uint2 a = *reinterpret_cast<const uint2*>(sf + p * 512 + upper);
+            const uint2 b = *reinterpret_cast<const uint2*>(sf + C::SF_BYTES + p * 512 + upper);
+            w[p] = make_uint4(a.x, a.y, b.x, b.y);
+          } else {
+            w[p] = *reinterpret_cast<const uint4*>(sf + p * 512);
+          }
+          const uint8_t* piece = sf + 2 * C::SF_BYTES + p * 512;
+          const uint4 a = *reinterpret_cast<const uint4*>(piece);
+          const uint4 b = two ? *reinterpret_cast<const uint4*>(piece + C::SF_BYTES) : make_uint4(0, 0, 0, 0);
+          r[p] = off ? make_uint4(a.z, a.w, b.x, b.y) : a;
+          r2[p] = off ? make_uint2(b.z, b.w) : make_uint2(b.x, b.y);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s.sempty[stage]);
+          w_ok = mbar_wait(&s.empty[before], before_phase, abort_flag) ? 1 : 0;
+        }
         w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
         if (!w_ok) { ok = false; break; }
         tc_fence_after();
-        const uint8_t* sf = s.ring[stage] + W_BYTES + C::T_BYTES;
         const uint32_t slot = tmem + quarter + C::SF_COL + (uint32_t)sl * C::SF_SLOT;
-        // pieces past the row's end hold an earlier stage's scales: written, never used
-        if (MODE == kSwiglu) {
-          // columns 0, 1: 64 gate rows, 2, 3: the same up rows
-#pragma unroll
-          for (int p = 0; p < CPS; ++p) {
-            const uint2 a = *reinterpret_cast<const uint2*>(sf + p * 512 + lane * 16 + upper);
-            const uint2 b = *reinterpret_cast<const uint2*>(sf + C::SF_BYTES + p * 512 + lane * 16 + upper);
-            tmem_st_x4(slot + 4 * p, make_uint4(a.x, a.y, b.x, b.y));
-          }
-        } else {
-          tmem_st_scales<CPS>(slot, sf, lane);
-        }
 #pragma unroll
         for (int p = 0; p < CPS; ++p) {
-          const uint8_t* piece = sf + 2 * C::SF_BYTES + p * 512 + lane * 16;
-          const uint4 a = *reinterpret_cast<const uint4*>(piece);
-          const uint4 b = two ? *reinterpret_cast<const uint4*>(piece + C::SF_BYTES) : make_uint4(0, 0, 0, 0);
-          const uint32_t col = slot + CPS * 4 + 6 * p;
-          tmem_st_x4(col, off ? make_uint4(a.z, a.w, b.x, b.y) : a);
-          tmem_st_x2(col + 4, off ? b.z : b.x, off ? b.w : b.y);
+          tmem_st_x4(slot + 4 * p, w[p]);
+          tmem_st_x4(slot + CPS * 4 + 6 * p, r[p]);
+          tmem_st_x2(slot + CPS * 4 + 6 * p + 4, r2[p].x, r2[p].y);
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         // like the accumulators, TMEM columns are handed over by the tcgen05 fences
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.sfull[sl]), 0));
-        if (++sl == C::SLOTS) sl = 0;
-        if (++before == STAGES) {
-          before = 0;
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.full[ostage]), 0));
+        ostage = ostage + 2 < STAGES ? ostage + 2 : set;
+        sl += 2;
+        if (sl >= C::SLOTS) sl -= C::SLOTS;
+        before += 2;
+        if (before >= STAGES) {
+          before -= STAGES;
           before_phase ^= 1u;
         }
-        if (++stage == STAGES) {
-          stage = 0;
+        stage += 2;
+        if (stage >= C::SF_STAGES) {
+          stage -= C::SF_STAGES;
           phase ^= 1u;
         }
       }
