@@ -1297,18 +1297,29 @@ int make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
 
 }  // namespace
 
+int make_tiled_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank,
+                   const uint64_t* dims, const uint64_t* strides, const uint32_t* box, bool swizzle) {
+  if (get_encoder() != MOE_OK) return MOE_ERR_CUDA;
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], e[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    e[i] = 1;
+    if (i + 1 < rank) s[i] = strides[i];
+  }
+  const CUresult r = g_encode(m, type, rank, const_cast<void*>(base), d, s, b, e,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
 int make_byte_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_bytes,
                   uint32_t box_rows) {
-  if (get_encoder() != MOE_OK) return MOE_ERR_CUDA;
-  const cuuint64_t dims[2] = {row_bytes, rows};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {128, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
-                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+  const uint64_t dims[2] = {row_bytes, rows}, strides[1] = {row_bytes};
+  const uint32_t box[2] = {128, box_rows};
+  return make_tiled_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 2, dims, strides, box, true);
 }
 
 namespace {

@@ -34,6 +34,10 @@ struct DeviceInfo {
 // Cached per device; returns MOE_OK, MOE_ERR_CUDA or MOE_ERR_NO_DEVICE.
 int current_device_info(DeviceInfo* info);
 
+// Tensor map of a tiled tensor of up to five dimensions, innermost first (strides in bytes, from the
+// second dimension on), with the 128-byte swizzle or none, zeros past the ends.
+int make_tiled_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank,
+                   const uint64_t* dims, const uint64_t* strides, const uint32_t* box, bool swizzle);
 // Tensor map of a row-major byte matrix: boxes of 128 bytes x box_rows rows, 128-byte swizzle,
 // zeros past the last row and past the row's end.
 int make_byte_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_bytes,

@@ -122,6 +122,7 @@ struct Pair {
   static constexpr int STAGE = W_BYTES + T_BYTES;
   static constexpr int STAGES = 6;
   static constexpr int SF_STAGE = 4 * SF_BYTES;            // gate and up (or W), the rows: two scale tiles
+  static constexpr int SF_BOX = CPS * 64;                  // a stage's pieces in 8-byte elements
   static constexpr int SF_STAGES = CPS == 4 ? 4 : 6;       // of a ring of their own
   static constexpr int SF_COL = 2 * NT;                    // after two accumulators
   static constexpr int SF_SLOT = CPS * 10;                 // W: CPS x 4, rows: CPS x 6
@@ -135,7 +136,7 @@ struct Pair {
 template <class C>
 struct alignas(1024) Storage {
   uint8_t ring[C::STAGES][C::STAGE];
-  alignas(16) uint8_t sring[C::SF_STAGES][C::SF_STAGE];
+  alignas(128) uint8_t sring[C::SF_STAGES][C::SF_STAGE];
   uint64_t full[C::STAGES];   // operands have landed; pair, on the leader: those of both CTAs, and the
                               // scales of both CTAs are in TMEM
   uint64_t empty[C::STAGES];
@@ -300,6 +301,24 @@ __device__ __forceinline__ uint32_t mbar_test(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok;
+}
+
+// Tiled TMA loads of more dimensions: for a CTA pair, counted on an mbarrier of either CTA (cluster
+// address), and plain ones.
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* tmap, int c0, int c1, int c2,
+                                                 uint32_t bar_cluster_addr) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar_cluster_addr)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int c0, int c1, int c2, int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
 }
 
 // Untiled bulk copy global -> shared, completion counted on `bar`; 16-byte aligned both sides.
@@ -729,8 +748,9 @@ __device__ __forceinline__ void range_bar(int third) { asm volatile("bar.sync %0
 
 template <int CPS, int MODE>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    k_mx4_gemm_pair(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmW64,
-                    const __grid_constant__ CUtensorMap tmA96, const __grid_constant__ CUtensorMap tmA16, const Args g) {
+    k_mx4_gemm_pair(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA96,
+                    const __grid_constant__ CUtensorMap tmA16, const __grid_constant__ CUtensorMap tmSW,
+                    const __grid_constant__ CUtensorMap tmSA, const Args g) {
   using C = Pair<CPS>;
   constexpr bool NV = CPS == 4;
   constexpr int STAGES = C::STAGES, NT = C::NT;
@@ -757,9 +777,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     s.abort_flag = 0;
     fence_barrier_init();
-    prefetch_tensormap(MODE == kSwiglu ? &tmW64 : &tmW);
+    prefetch_tensormap(&tmW);
     prefetch_tensormap(&tmA96);
     prefetch_tensormap(&tmA16);
+    prefetch_tensormap(&tmSW);
+    prefetch_tensormap(&tmSA);
   }
   pdl_wait();
   __syncthreads();
@@ -779,30 +801,32 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
   // whole warps in step with one lane issuing, as in k_mx4_gemm
   if (warp == 0) {
-    // ---- TMA producer of the operands (both CTAs), counted on the leader -----------------------
+    // ---- TMA producer of the operands (both CTAs), counted on the leader. A thread issues a copy every
+    // 140 cycles or so, whatever its size: two copies per stage here and two of scales below
+    // (one thread for all seven plain ones took 600 us for 32768 rows) -----------------------------
     int stage = 0;
     uint32_t phase = 0;
+    uint32_t ready = 0;          // the coming stage was seen to be empty
     bool ok = true;
     for (int tile = cluster; ok && tile < total; tile += nclusters) {
       const Tile t = decode(s, g, tile, NT);
       const int mine = ((uni(t.n) + 31) & ~31) / 2;          // rows of this CTA's half
       const int arow = uni(t.row0) + mine * (int)rank;
-      // this CTA's first weight row; past the group's end (an odd number of 128-row blocks)
-      // the boxes read on or are zeros: those channels are dropped
-      const int wrow = uni(t.g) * g.w_rows + uni(t.n0) + (MODE == kSwiglu ? 64 : 128) * (int)rank;
+      const int grp = uni(t.g);
+      // this CTA's first weight row in its group; past the group's end (an odd number of 128-row
+      // blocks) the boxes read on or are zeros: those channels are dropped
+      const int wl = uni(t.n0) + (MODE == kSwiglu ? 64 : 128) * (int)rank;
       for (int kb = 0; kb < g.kstages; ++kb) {
-        ok = warp_wait(&s.empty[stage], phase ^ 1u, abort_flag);
+        if (!__all_sync(0xffffffffu, ready)) ok = warp_wait(&s.empty[stage], phase ^ 1u, abort_flag);
         if (!ok) break;
+        const int next = stage + 1 == STAGES ? 0 : stage + 1;
+        ready = mbar_test(&s.empty[next], next ? phase ^ 1u : phase);
         if (elect_one()) {
           uint8_t* st = s.ring[stage];
           const uint32_t full = mapa_shared(smem_u32(&s.full[stage]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * (W_BYTES + mine * 128));
-          if (MODE == kSwiglu) {
-            tma_load_2d_pair(st, &tmW64, kb * 128, wrow, full);
-            tma_load_2d_pair(st + W_BYTES / 2, &tmW64, kb * 128, wrow + g.w_second, full);
-          } else {
-            tma_load_2d_pair(st, &tmW, kb * 128, wrow, full);
-          }
+          if (MODE == kSwiglu) tma_load_3d_pair(st, &tmW, kb * 128, wl, 2 * grp, full);
+          else tma_load_2d_pair(st, &tmW, kb * 128, grp * g.w_rows + wl, full);
           uint8_t* rows = st + W_BYTES;
           if (mine == NT / 2) {
             tma_load_2d_pair(rows, &tmA96, kb * 128, arow, full);
@@ -811,46 +835,42 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         }
         __syncwarp();
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        stage = next;
+        if (next == 0) phase ^= 1u;
       }
     }
   } else if (warp == kScaleProducer) {
     // ---- TMA producer of the scales, counted on this CTA, into a ring that the scale warps free
-    // as soon as they have read a stage ----------------------------------------------------------
+    // as soon as they have read a stage. Always two scale tiles of rows: what the tile does not have
+    // of them is any group's or zeros, and not used ----------------------------------------------
     int stage = 0;
     uint32_t phase = 0;
+    uint32_t ready = 0;
     bool ok = true;
     for (int tile = cluster; ok && tile < total; tile += nclusters) {
       const Tile t = decode(s, g, tile, NT);
-      const int grp = uni(t.g), o_g = uni(t.o_g), l0 = uni(t.row0) - o_g;
-      const int sft = ((l0 & 127) + uni(t.n) + 127) / 128;   // scale tiles of all the rows
-      const int64_t wo = (int64_t)grp * g.w_rows;
-      const int wl = uni(t.n0) + (MODE == kSwiglu ? 64 : 128) * (int)rank;
-      const uint8_t* sw = scale_tile(g.w_scales, wo, grp, min(wl, g.w_rows - 1), g.chunks);
-      const uint8_t* sw2 = scale_tile(g.w_scales, wo, grp, wl + g.w_second, g.chunks);     // kSwiglu
-      const uint8_t* sa = scale_tile(g.a_scales, o_g, grp, l0, g.chunks);
+      const int grp = uni(t.g), o_g = uni(t.o_g);
+      const int ta = (o_g >> 7) + grp + ((uni(t.row0) - o_g) >> 7);
+      // kSwiglu: the tile of the 128 channels; else the CTA's own one, the group's last one where the
+      // CTA has no channels
+      const int wl = uni(t.n0) + (MODE == kSwiglu ? 0 : min(128 * (int)rank, g.w_rows - 1 - uni(t.n0)));
+      const int tw = MODE == kSwiglu ? wl >> 7 : (int)(((int64_t)grp * g.w_rows) >> 7) + grp + (wl >> 7);
       for (int kb = 0; kb < g.kstages; ++kb) {
-        ok = warp_wait(&s.sempty[stage], phase ^ 1u, abort_flag);
+        if (!__all_sync(0xffffffffu, ready)) ok = warp_wait(&s.sempty[stage], phase ^ 1u, abort_flag);
         if (!ok) break;
+        const int next = stage + 1 == C::SF_STAGES ? 0 : stage + 1;
+        ready = mbar_test(&s.sempty[next], next ? phase ^ 1u : phase);
         if (elect_one()) {
           uint8_t* sf = s.sring[stage];
           uint64_t* bar = &s.sland[stage];
-          const uint32_t sfb = 512u * (uint32_t)min(CPS, g.chunks - kb * CPS);
-          const size_t at = (size_t)kb * CPS * 512;
-          mbar_arrive_expect_tx(bar, sfb * ((MODE == kSwiglu ? 2 : 1) + sft));
-          bulk_load(sf, sw + at, sfb, bar);
-          if (MODE == kSwiglu) bulk_load(sf + C::SF_BYTES, sw2 + at, sfb, bar);
-          for (int i = 0; i < sft; ++i)
-            bulk_load(sf + (2 + i) * C::SF_BYTES, sa + (size_t)i * g.chunks * 512 + at, sfb, bar);
+          mbar_arrive_expect_tx(bar, C::SF_BYTES * (MODE == kSwiglu ? 4 : 3));
+          if (MODE == kSwiglu) tma_load_4d(sf, &tmSW, kb * C::SF_BOX, tw, 0, grp, bar);
+          else tma_load_2d(sf, &tmSW, kb * C::SF_BOX, tw, bar);
+          tma_load_2d(sf + 2 * C::SF_BYTES, &tmSA, kb * C::SF_BOX, ta, bar);
         }
         __syncwarp();
-        if (++stage == C::SF_STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        stage = next;
+        if (next == 0) phase ^= 1u;
       }
     }
   } else if (warp == 1) {
@@ -1084,11 +1104,31 @@ template <int CPS, int MODE>
 int launch_pair(const moe_mx4_t& a, const moe_mx4_t& w, const Args& g, const DeviceInfo& dev, cudaStream_t st) {
   constexpr size_t smem = sizeof(Storage<Pair<CPS>>) + 1024;
   static_assert(smem <= 227 * 1024 && Pair<CPS>::STAGES >= 3, "shared memory budget");
-  CUtensorMap mw, w64, a96, a16;
-  MOE_TRY(make_byte_map(&mw, w.codes, (uint64_t)w.rows, a.K / 2, 128));
-  MOE_TRY(make_byte_map(&w64, w.codes, (uint64_t)w.rows, a.K / 2, 64));
-  MOE_TRY(make_byte_map(&a96, a.codes, (uint64_t)a.rows, a.K / 2, 96));
-  MOE_TRY(make_byte_map(&a16, a.codes, (uint64_t)a.rows, a.K / 2, 16));
+  CUtensorMap mw, a96, a16, sw, sa;
+  const uint64_t half = a.K / 2, piece_row = (uint64_t)g.chunks * 512;
+  const CUtensorMapDataType eight = CU_TENSOR_MAP_DATA_TYPE_FLOAT64;    // 8 bytes an element: boxes of 256
+  if (MODE == kSwiglu) {
+    // [groups, gate | up, I rows]: one box has 64 gate rows and the same up rows
+    const uint64_t I = g.n_out, tiles = I / 128;
+    const uint64_t wd[3] = {half, I, 2ull * w.groups}, ws[2] = {half, I * half};
+    const uint32_t wb[3] = {128, 64, 2};
+    MOE_TRY(make_tiled_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, 3, wd, ws, wb, true));
+    // a group has 2 I / 128 scale tiles and one to spare
+    const uint64_t sd[4] = {piece_row / 8, tiles, 2, (uint64_t)w.groups};
+    const uint64_t ss[3] = {piece_row, tiles * piece_row, (2 * tiles + 1) * piece_row};
+    const uint32_t sb[4] = {Pair<CPS>::SF_BOX, 1, 2, 1};
+    MOE_TRY(make_tiled_map(&sw, eight, w.scales, 4, sd, ss, sb, false));
+  } else {
+    MOE_TRY(make_byte_map(&mw, w.codes, (uint64_t)w.rows, half, 128));
+    const uint64_t sd[2] = {piece_row / 8, mx4_scale_tiles(w)}, ss[1] = {piece_row};
+    const uint32_t sb[2] = {Pair<CPS>::SF_BOX, 1};
+    MOE_TRY(make_tiled_map(&sw, eight, w.scales, 2, sd, ss, sb, false));
+  }
+  MOE_TRY(make_byte_map(&a96, a.codes, (uint64_t)a.rows, half, 96));
+  MOE_TRY(make_byte_map(&a16, a.codes, (uint64_t)a.rows, half, 16));
+  const uint64_t ad[2] = {piece_row / 8, mx4_scale_tiles(a)}, as[1] = {piece_row};
+  const uint32_t ab[2] = {Pair<CPS>::SF_BOX, 2};
+  MOE_TRY(make_tiled_map(&sa, eight, a.scales, 2, ad, as, ab, false));
   auto kern = k_mx4_gemm_pair<CPS, MODE>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return MOE_ERR_CUDA;
@@ -1120,7 +1160,7 @@ int launch_pair(const moe_mx4_t& a, const moe_mx4_t& w, const Args& g, const Dev
     }
     n = clusters_of[dev.device];
   }
-  const cudaError_t e = launch_kernel(kern, 2 * n, kPairThreads, smem, st, 2, mw, w64, a96, a16, g);
+  const cudaError_t e = launch_kernel(kern, 2 * n, kPairThreads, smem, st, 2, mw, a96, a16, sw, sa, g);
   count_launch();
   return cuda_rc(e);
 }
