@@ -23,11 +23,11 @@
 // Warps:
 //   0           TMA producer: per stage of K = 256 elements (128 bytes, 128-byte swizzle) the
 //               weight boxes, the tile's rows in a few boxes, and (in the pair kernel a warp of
-//               its own, 22) the block scales as plain bulk copies of the 512-byte pieces
+//               its own, 18) the block scales as plain bulk copies of the 512-byte pieces
 //   1           TMEM owner and MMA issuer (the pair's leader): 4 tcgen05.mma of K = 64 per stage
 //               and weight block
-//   2-13        epilogue: tcgen05.ld, math, global stores
-//   14-17       scales (pair: 14-21, four warps for every other stage): each warp copies the stage's pieces from shared memory to its lane quarter
+//   2-9         epilogue: tcgen05.ld, math, global stores
+//   10-13       scales (pair: 10-17, four warps for every other stage): each warp copies the stage's pieces from shared memory to its lane quarter
 //               of TMEM with tcgen05.st (the MMA reads them in all four quarters)
 // The scales of the stages take turns over the TMEM columns that are left, 3 to 5 slots: with fewer
 // slots than stages the scale warps wait, before they overwrite a slot, until the MMAs that read it
@@ -58,7 +58,9 @@
 namespace moe {
 namespace {
 
-constexpr int kEpiWarps = 12;                       // three per TMEM lane quarter
+// two per TMEM lane quarter; a third one gains nothing, and its issue slots are missed by the
+// producers and the issuer (387 us instead of 361 at 32768 rows)
+constexpr int kEpiWarps = 8;
 constexpr int kScaleWarps = 4;
 constexpr int kThreads = 64 + (kEpiWarps + kScaleWarps) * 32;
 constexpr int kScaleProducer = 2 + kEpiWarps + 2 * kScaleWarps;    // pair kernel: 8 scale warps, and one more
@@ -636,10 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---- epilogue: TMEM lane quarter = warp % 4; the three warps of a quarter take turns over
+    // ---- epilogue: TMEM lane quarter = warp % 4; the two warps of a quarter take turns over
     // chunks of 16 columns ----------------------------------------------------------------------
     const int q = warp & 3;
-    const int third = (warp - 2) >> 2;
+    const int part = (warp - 2) >> 2;
     float (*stg)[kStageLd] = reinterpret_cast<float (*)[kStageLd]>(s.turn + (warp - 2) * 8 * kStageLd);
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 2 * NT);
       const int ch = t.n0 + 32 * q + (lane & ~7);
 #pragma unroll 1
-      for (int c = 16 * third; c < t.n; c += 16 * (kEpiWarps / 4)) {
+      for (int c = 16 * part; c < t.n; c += 16 * (kEpiWarps / 4)) {
         uint32_t v[2][16];
         tmem_ld_32x32b_x16(base + c, v[0]);
         tmem_ld_32x32b_x16(base + NT + c, v[1]);
@@ -743,8 +745,8 @@ __device__ __forceinline__ void epi_round_h_pair(const Args& a, const Tile& t, i
   }
 }
 
-// The epilogue warps of one column range (four warps) meet here; named barriers 1 to 3.
-__device__ __forceinline__ void range_bar(int third) { asm volatile("bar.sync %0, 128;" ::"r"(third + 1) : "memory"); }
+// The epilogue warps of one column range (four warps) meet here; named barriers 1 and 2.
+__device__ __forceinline__ void range_bar(int part) { asm volatile("bar.sync %0, 128;" ::"r"(part + 1) : "memory"); }
 
 template <int CPS, int MODE>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -1007,12 +1009,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     }
   } else {
-    // ---- epilogue (both CTAs): this CTA's 128 weight rows; the three warps of a quarter take
+    // ---- epilogue (both CTAs): this CTA's 128 weight rows; the two warps of a quarter take
     // turns over chunks of 16 columns -----------------------------------------------------------
     const int q = warp & 3;
-    const int third = (warp - 2) >> 2;
+    const int part = (warp - 2) >> 2;
     float (*stg)[kStageLd] = reinterpret_cast<float (*)[kStageLd]>(s.turn + (warp - 2) * 8 * kStageLd);
-    float (*S)[kGroupLd] = reinterpret_cast<float (*)[kGroupLd]>(s.turn + third * 8 * kGroupLd);
+    float (*S)[kGroupLd] = reinterpret_cast<float (*)[kGroupLd]>(s.turn + part * 8 * kGroupLd);
     int acc = 0;
     uint32_t acc_phase = 0;
     const float af = NV && g.a_factor ? *g.a_factor : 1.0f;
@@ -1027,15 +1029,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       // all four warps of a range leave together: they meet at its barrier
       if (MODE == kSwiglu) {
         if (lane == 0) s.turn_ok[warp - 2] = w_ok;
-        range_bar(third);
-        w_ok = s.turn_ok[4 * third] & s.turn_ok[4 * third + 1] & s.turn_ok[4 * third + 2] & s.turn_ok[4 * third + 3];
-        range_bar(third);
+        range_bar(part);
+        w_ok = s.turn_ok[4 * part] & s.turn_ok[4 * part + 1] & s.turn_ok[4 * part + 2] & s.turn_ok[4 * part + 3];
+        range_bar(part);
       }
       if (!w_ok) break;
       tc_fence_after();
       const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * NT);
 #pragma unroll 1
-      for (int c = 16 * third; c < t.n; c += 16 * (kEpiWarps / 4)) {
+      for (int c = 16 * part; c < t.n; c += 16 * (kEpiWarps / 4)) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(base + c, v);
         tmem_ld_wait();
@@ -1044,9 +1046,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           for (int e = 0; e < 16; e += 8) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) S[j][32 * q + lane] = __uint_as_float(v[e + j]);
-            range_bar(third);
+            range_bar(part);
             epi_round_h_pair<NV>(g, t, c + e, t.n0 + 64 * (int)rank, q, lane, f, S, hf, inv6);
-            range_bar(third);                         // the rows may be written again
+            range_bar(part);                         // the rows may be written again
           }
         } else {
 #pragma unroll
