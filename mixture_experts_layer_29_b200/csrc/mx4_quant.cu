@@ -81,15 +81,6 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const QuantArgs 
   }
   unsigned left = __ballot_sync(0xffffffffu, dst >= 0);
   if (!left) return;
-  float f = 1.0f;
-  int g = -1, o_g = 0, row = -1;
-  if (!q.row_of) {      // one destination: a row of no group is not read
-    row = t;
-    g = mx4_find_group(q.m, row, o_g);
-    if (g < 0) return;
-  }
-  if (NV && q.factor) f = q.factor[q.factor_per_group ? g : 0];
-
   const T* src = static_cast<const T*>(q.x) + (int64_t)t * q.ld;
   float v[kSeg][8];
 #pragma unroll
@@ -102,6 +93,15 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const QuantArgs 
       for (int i = 0; i < 8; ++i) v[s][i] = 0.f;
     }
   }
+  float f = 1.0f;
+  int g = -1, o_g = 0, row = -1;
+  if (!q.row_of) {      // one destination: its group is looked for while the loads are under way
+    row = t;
+    g = mx4_find_group(q.m, row, o_g);
+    if (g < 0) return;
+  }
+  if (NV && q.factor) f = q.factor[q.factor_per_group ? g : 0];
+
   uint32_t code[kSeg], scale[kSeg];
 #pragma unroll
   for (int s = 0; s < kSeg; ++s) {
@@ -112,10 +112,10 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const QuantArgs 
     for (int o = 1; o < mx4_block(NV) / 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     float by;
     const uint32_t byte = mx4_scale<NV>(top, f, by);
+    mx4_scaled<NV>(v[s], by);
     uint32_t c = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c |= e2m1x2(mx4_scaled<NV>(v[s][2 * i], by), mx4_scaled<NV>(v[s][2 * i + 1], by)) << (8 * i);
+    for (int i = 0; i < 4; ++i) c |= e2m1x2(v[s][2 * i], v[s][2 * i + 1]) << (8 * i);
     code[s] = c;
     // the four scales of one piece's row, gathered from its 16 (8) lanes into a word
     constexpr int kLanes = mx4_block(NV) / 8;
