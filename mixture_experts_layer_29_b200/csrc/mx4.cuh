@@ -89,48 +89,71 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte) {
   return __uint_as_float(byte == 255u ? 0x7FC00000u : byte ? byte << 23 : 1u << 22);
 }
 
-// A block's scale byte, and what its elements are divided (NVFP4) or multiplied (MXFP4) by
-// before rounding, from the bits of the block's largest magnitude (as unsigned integers the
-// magnitudes of floats are in order, and those of infinity and NaN are the largest). `by` is 0
-// where every element rounds to 0: an empty block, or one without a finite scale.
+// max(a, |b|) of non-negative a, NaN if either is one.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+// The correctly rounded quotient x / d from r, the correctly rounded reciprocal of d: with t = x r it
+// is t + r (x - t d) (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) while nothing underflows. 3 operations for a division's dozen.
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+  const float t = __fmul_rn(x, r);
+  return __fmaf_rn(r, __fmaf_rn(-t, d, x), t);
+}
+// d for which quotient() is good: an x so small beside it that x - t d underflows has a quotient
+// below 2^-40, which rounds to 0 on every grid here.
+__device__ __forceinline__ bool quotient_ok(float d) { return d >= 0x1p-60f && d <= 0x1p60f; }
+
+// t of an NVFP4 matrix with what its scales are made with.
+struct Mx4Factor {
+  float t, six, r;         // t, 6 t, 1 / (6 t)
+};
+__device__ __forceinline__ Mx4Factor mx4_factor(float t) {
+  const float six = __fmul_rn(6.0f, t);
+  return Mx4Factor{t, six, __frcp_rn(six)};
+}
+
+// A block's scale byte, and what its elements are divided (NVFP4) or multiplied (MXFP4) by before
+// rounding, from the block's largest magnitude. `by` is 0 where every element becomes 0: an empty
+// NVFP4 block, or a block without a finite scale.
 template <bool NV>
-__device__ __forceinline__ uint32_t mx4_scale(uint32_t amax_bits, float t, float& by) {
+__device__ __forceinline__ uint32_t mx4_scale(float amax, const Mx4Factor& f, float& by) {
+  const uint32_t bits = __float_as_uint(amax);
   by = 0.f;
   if (NV) {
-    if (amax_bits >= 0x7F800000u) return 0x7Fu;
-    const uint32_t s = e4m3(__fdiv_rn(__uint_as_float(amax_bits), __fmul_rn(6.0f, t)));
-    if (s != 0u) by = __fmul_rn(e4m3_value(s), t);
+    if (bits >= 0x7F800000u) return 0x7Fu;
+    const uint32_t s = e4m3(quotient_ok(f.six) ? quotient(amax, f.six, f.r) : __fdiv_rn(amax, f.six));
+    by = __fmul_rn(e4m3_value(s), f.t);
     return s;
   }
-  const uint32_t e = amax_bits >> 23;
+  const uint32_t e = bits >> 23;
   if (e == 255u) return 255u;
   const uint32_t b = e > 2u ? e - 2u : 0u;
   by = __uint_as_float((254u - b) << 23);
   return b;
 }
-// The elements of a block on its grid, before rounding. NVFP4 divides by `by`: with r the correctly
-// rounded reciprocal and t = x r, t + r (x - t by) is the correctly rounded quotient (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990) while nothing
-// underflows: for by in [2^-60, 2^60]; an x so small beside it that x - t by does is far below the
-// smallest element. That is 3 operations an element for a division's dozen.
-template <bool NV, int N>
-__device__ __forceinline__ void mx4_scaled(float (&x)[N], float by) {
-  if (NV) {
-    if (by >= 0x1p-60f && by <= 0x1p60f) {
-      const float r = __frcp_rn(by);
+// The codes of 8 elements of a block (the first in the low bits).
+template <bool NV>
+__device__ __forceinline__ uint32_t mx4_codes(const float (&x)[8], float by) {
+  float q[8];
+  if (!NV) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float t = __fmul_rn(x[i], r);
-        x[i] = __fmaf_rn(r, __fmaf_rn(-t, by, x[i]), t);
-      }
-    } else {
+    for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(x[i], by);
+  } else if (quotient_ok(by)) {
+    const float r = __frcp_rn(by);
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = by != 0.f ? __fdiv_rn(x[i], by) : 0.f;
-    }
+    for (int i = 0; i < 8; ++i) q[i] = quotient(x[i], by, r);
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = by != 0.f ? __fmul_rn(x[i], by) : 0.f;   // (inf or NaN) * 0 would not be 0
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], by);
   }
+  uint32_t c = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c |= e2m1x2(q[2 * i], q[2 * i + 1]) << (8 * i);
+  return by != 0.f ? c : 0u;
 }
 
 // ---- host side -------------------------------------------------------------------------------

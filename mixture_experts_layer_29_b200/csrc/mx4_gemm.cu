@@ -351,7 +351,7 @@ __device__ __forceinline__ void turn_around(float (&v)[8], float (*stg)[kStageLd
 // units in its last place at most.
 template <bool NV>
 __device__ __forceinline__ uint32_t round_scale(uint32_t top, float hf, float inv6, float& by) {
-  if (!NV) return mx4_scale<false>(top, 1.0f, by);
+  if (!NV) return mx4_scale<false>(__uint_as_float(top), Mx4Factor{}, by);
   by = 0.f;
   if (top >= 0x7F800000u) return 0x7Fu;
   const uint32_t byte = e4m3(__uint_as_float(top) * inv6);
