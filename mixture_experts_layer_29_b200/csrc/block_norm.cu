@@ -184,8 +184,34 @@ struct BwdArgs {
   float* partial;        // [grid, 3, H]: d_w_post, d_w_pre, d_gate (the parts that exist)
 };
 
+// A token's rows as they are loaded.
+template <int VPT>
+struct RawRows {
+  uint4 d[VPT], n[VPT], r[VPT], b[VPT];
+  float rr, rb;
+};
 template <typename T, int VPT>
-__global__ void __launch_bounds__(1024) k_block_norm_bwd(const BwdArgs a) {
+__device__ __forceinline__ void load_rows(const BwdArgs& a, size_t t, int nvec, RawRows<VPT>& q) {
+  const size_t o = t * a.H;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const auto vec = [&](const void* p, int v) { return reinterpret_cast<const uint4*>(static_cast<const T*>(p) + o)[v]; };
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    const bool in = v < nvec;
+    q.n[i] = in && a.w_pre ? vec(a.d_normed, v) : zero;
+    q.r[i] = in && a.w_pre ? vec(a.res_out, v) : zero;
+    q.d[i] = in && a.d_res_out ? vec(a.d_res_out, v) : zero;
+    q.b[i] = in && a.block ? vec(a.block, v) : zero;
+  }
+  q.rr = a.w_pre ? a.rstd_res[t] : 0.f;
+  q.rb = a.w_post ? a.rstd_block[t] : 1.f;
+}
+
+// MAXT: most threads of a CTA. A CTA of a wide row has an SM to itself (its sums take 24 registers per
+// 8 columns), so it loads the next token's rows before it works on the ones it has.
+template <typename T, int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_block_norm_bwd(const BwdArgs a) {
   constexpr int N = Row<T>::N;
   __shared__ float part[2][32];
   pdl_launch_dependents();
@@ -198,25 +224,21 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd(const BwdArgs a) {
 #pragma unroll
     for (int j = 0; j < N; ++j) sw_post[i][j] = sw_pre[i][j] = s_gate[i][j] = 0.f;
 
+  RawRows<VPT> q;
+  if (blockIdx.x < (unsigned)a.T) load_rows<T, VPT>(a, blockIdx.x, nvec, q);
   for (size_t t = blockIdx.x; t < (size_t)a.T; t += gridDim.x) {
     const size_t o = t * a.H;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
     uint4 qd[VPT], qb[VPT];
     float g[VPT][N], rhat[VPT][N], sum = 0.f;
-    float rr = 0.f, rb = 1.f;
-    if (a.w_pre) rr = a.rstd_res[t];
-    if (a.w_post) rb = a.rstd_block[t];
+    const float rr = q.rr, rb = q.rb;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      const bool in = v < nvec;
-      qd[i] = in && a.d_res_out ? reinterpret_cast<const uint4*>(static_cast<const T*>(a.d_res_out) + o)[v] : zero;
-      qb[i] = in && a.block ? reinterpret_cast<const uint4*>(static_cast<const T*>(a.block) + o)[v] : zero;
-      const uint4 qn = in && a.w_pre ? reinterpret_cast<const uint4*>(static_cast<const T*>(a.d_normed) + o)[v] : zero;
-      const uint4 qr = in && a.w_pre ? reinterpret_cast<const uint4*>(static_cast<const T*>(a.res_out) + o)[v] : zero;
-      Row<T>::unpack(qn, g[i]);
-      Row<T>::unpack(qr, rhat[i]);
+      Row<T>::unpack(q.n[i], g[i]);
+      Row<T>::unpack(q.r[i], rhat[i]);
+      qd[i] = q.d[i];
+      qb[i] = q.b[i];
     }
+    if (t + gridDim.x < (size_t)a.T) load_rows<T, VPT>(a, t + gridDim.x, nvec, q);
     if (a.w_pre) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
@@ -304,28 +326,27 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd(const BwdArgs a) {
   }
 }
 
-// out[k][c] = sum over the CTAs' partial sums in order, for the arrays that are wanted.
-__global__ void __launch_bounds__(256) k_block_norm_sum(const float* partial, int n, int H, float* w_post,
-                                                        float* w_pre, float* gate) {
+// out[k][c] = sum over the CTAs' partial sums, for the arrays that are wanted: 32 columns per block,
+// whose 32 warps share the CTAs; each warp adds its ones in order, then the warps' sums in order.
+__global__ void __launch_bounds__(1024) k_block_norm_sum(const float* partial, int n, int H, float* w_post,
+                                                         float* w_pre, float* gate) {
   pdl_launch_dependents();
   pdl_wait();
   float* out = blockIdx.y == 0 ? w_post : blockIdx.y == 1 ? w_pre : gate;
   if (!out) return;
-  __shared__ float part[8][33];
-  // 32 columns per block, 8 warps share the CTAs
+  __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < H)
-    for (int i = warp; i < n; i += 8) s += partial[((size_t)i * 3 + blockIdx.y) * H + c];
-  part[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < H) {
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += part[i][lane];
-    out[c] = s;
+  if (c < H) {
+#pragma unroll 4
+    for (int i = warp; i < n; i += 32) s += partial[((size_t)i * 3 + blockIdx.y) * H + c];
   }
+  part[lane][warp] = s;
+  __syncthreads();
+  // warp w adds up column w
+  const float v = warp_sum_f(part[warp][lane]);
+  if (lane == 0 && blockIdx.x * 32 + warp < H) out[blockIdx.x * 32 + warp] = v;
 }
 
 int check_norm(const moe_norm_t* n) {
@@ -338,17 +359,22 @@ int check_norm(const moe_norm_t* n) {
   return MOE_OK;
 }
 
-// Threads of a row's CTA and the vectors each holds: whole warps, `most` threads at most.
+// Threads of a row's CTA and the vectors each holds (1 to 4): whole warps, `most` threads where four
+// vectors suffice for that, else up to 1024.
 void row_shape(int nvec, int most, int* vpt, int* threads) {
-  int v = 1;
-  while ((nvec + v - 1) / v > most) v *= 2;
-  *vpt = v;
-  *threads = ((nvec + v - 1) / v + 31) / 32 * 32;
+  if (nvec > 4 * most) most = 1024;
+  *vpt = (nvec + most - 1) / most;
+  *threads = ((nvec + *vpt - 1) / *vpt + 31) / 32 * 32;
 }
 
-// Persistent CTAs of the backward: a row's threads, as many as a full SM's registers allow.
-int bwd_grid(const moe_norm_t& n, int sm_count) { return min(n.T, 2 * sm_count); }
-constexpr int kMaxBwdGrid = 2 * 256;
+// The backward's CTAs: up to 768 threads a row (the register file holds 768 with their sums), and as
+// many CTAs as make up 768 threads per SM.
+constexpr int kBwdThreads = 768;
+void bwd_shape(const moe_norm_t& n, int* vpt, int* threads, int* per_sm) {
+  row_shape(n.H / (n.dtype == MOE_BF16 ? 8 : 4), kBwdThreads, vpt, threads);
+  *per_sm = max(1, kBwdThreads / *threads);
+}
+constexpr int kMaxSms = 256;
 
 }  // namespace
 }  // namespace moe
@@ -375,11 +401,13 @@ int moe_block_norm(const moe_norm_t* n, const void* residual, const void* block,
   FwdArgs a{n->H, n->gate, n->eps, n->scale, residual, block, w_post, gate, w_pre, residual_out, normed,
             rstd_block, rstd_res};
   const bool bf16 = n->dtype == MOE_BF16;
+  // few tokens: many threads per row, for the shortest way through; more: 256, so that an SM has
+  // several rows under way (8192 x 6144 bf16: 108, 82, 73, 75 us with 768, 384, 256, 192 threads)
   int vpt, threads;
-  row_shape(n->H / (bf16 ? 8 : 4), 1024, &vpt, &threads);
-  void (*kern)(FwdArgs) =
-      bf16 ? (vpt == 1 ? k_block_norm<__nv_bfloat16, 1> : k_block_norm<__nv_bfloat16, 2>)
-           : (vpt == 1 ? k_block_norm<float, 1> : vpt == 2 ? k_block_norm<float, 2> : k_block_norm<float, 4>);
+  row_shape(n->H / (bf16 ? 8 : 4), n->T > 2 * dev.sm_count ? 256 : 1024, &vpt, &threads);
+#define NORM_VPT(T) \
+  (vpt == 1 ? k_block_norm<T, 1> : vpt == 2 ? k_block_norm<T, 2> : vpt == 3 ? k_block_norm<T, 3> : k_block_norm<T, 4>)
+  void (*kern)(FwdArgs) = bf16 ? NORM_VPT(__nv_bfloat16) : NORM_VPT(float);
   const cudaError_t e = launch_kernel(kern, n->T, threads, 0, as_stream(stream), 1, a);
   count_launch();
   return cuda_rc(e);
@@ -388,7 +416,9 @@ int moe_block_norm(const moe_norm_t* n, const void* residual, const void* block,
 int moe_block_norm_workspace_size(const moe_norm_t* n, size_t* bytes) {
   MOE_TRY(check_norm(n));
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  *bytes = (size_t)kMaxBwdGrid * 3 * n->H * sizeof(float);
+  int vpt, threads, per_sm;
+  bwd_shape(*n, &vpt, &threads, &per_sm);
+  *bytes = (size_t)max(1, min(n->T, kMaxSms * per_sm)) * 3 * n->H * sizeof(float);
   return MOE_OK;
 }
 
@@ -427,19 +457,21 @@ int moe_block_norm_backward(const moe_norm_t* n, const void* d_residual_out, con
             rstd_block, rstd_res, d_residual, d_block, n->gate == MOE_GATE_TOKEN ? d_gate : nullptr,
             static_cast<float*>(ws)};
   const bool bf16 = n->dtype == MOE_BF16;
-  int vpt, threads;
-  row_shape(n->H / (bf16 ? 8 : 4), 1024, &vpt, &threads);
-  void (*kern)(BwdArgs) =
-      bf16 ? (vpt == 1 ? k_block_norm_bwd<__nv_bfloat16, 1> : k_block_norm_bwd<__nv_bfloat16, 2>)
-           : (vpt == 1 ? k_block_norm_bwd<float, 1> : vpt == 2 ? k_block_norm_bwd<float, 2> : k_block_norm_bwd<float, 4>);
-  const int grid = min(bwd_grid(*n, dev.sm_count), kMaxBwdGrid);
+  int vpt, threads, per_sm;
+  bwd_shape(*n, &vpt, &threads, &per_sm);
+#define NORM_BWD(T, MAXT)                                                            \
+  (vpt == 1 ? k_block_norm_bwd<T, 1, MAXT> : vpt == 2 ? k_block_norm_bwd<T, 2, MAXT> \
+   : vpt == 3 ? k_block_norm_bwd<T, 3, MAXT> : k_block_norm_bwd<T, 4, MAXT>)
+  void (*kern)(BwdArgs) = threads > kBwdThreads ? (bf16 ? NORM_BWD(__nv_bfloat16, 1024) : NORM_BWD(float, 1024))
+                                                : (bf16 ? NORM_BWD(__nv_bfloat16, kBwdThreads) : NORM_BWD(float, kBwdThreads));
+  const int grid = min(n->T, min(dev.sm_count, kMaxSms) * per_sm);
   if (n->T > 0) {
     MOE_TRY(cuda_rc(launch_kernel(kern, grid, threads, 0, st, 1, a)));
     count_launch();
   }
   float* chan = n->gate == MOE_GATE_CHANNEL ? d_gate : nullptr;
   if (!d_w_post && !d_w_pre && !chan) return MOE_OK;
-  const cudaError_t e = launch_kernel(k_block_norm_sum, dim3((n->H + 31) / 32, 3), 256, 0, st, 1,
+  const cudaError_t e = launch_kernel(k_block_norm_sum, dim3((n->H + 31) / 32, 3), 1024, 0, st, 1,
                                       static_cast<const float*>(ws), grid, n->H, d_w_post, d_w_pre, chan);
   count_launch();
   return cuda_rc(e);
