@@ -65,7 +65,8 @@ int moe_block_norm(const moe_norm_t* n, const void* residual, const void* block,
  * Outputs: d_residual [T, H] dtype, d_block [T, H] dtype, d_w_post [H], d_w_pre [H] and d_gate
  * ([T] or [H]) fp32, written, each for the parts the forward had and NULL otherwise. The sums
  * over tokens go in a fixed order: bit-reproducible.
- *   ws  device, >= moe_block_norm_workspace_size bytes; calls that run at once need one each */
+ *   ws  device, >= moe_block_norm_workspace_size bytes, zeroed before first use (status word, read
+ *       with moe_read_device_status; partial sums); calls that run at once need one each */
 int moe_block_norm_workspace_size(const moe_norm_t* n, size_t* bytes);
 int moe_block_norm_backward(const moe_norm_t* n, const void* d_residual_out, const void* d_normed,
                             const void* residual_out, const void* block, const float* w_post,

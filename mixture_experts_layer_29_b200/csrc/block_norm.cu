@@ -180,173 +180,288 @@ struct BwdArgs {
   const void *d_res_out, *d_normed, *res_out, *block;
   const float *w_post, *g, *w_pre, *rstd_block, *rstd_res;
   void *d_residual, *d_block;
-  float* d_gate;         // per token: written here; per channel: through the partial sums
-  float* partial;        // [grid, 3, H]: d_w_post, d_w_pre, d_gate (the parts that exist)
+  float* d_gate;         // per token
+  float* partial;        // [grid, 2, H]: sum of gate_t g bhat and of d_normed rhat (the parts that exist)
+  int* status;
 };
 
-// A token's rows as they are loaded.
-template <int VPT>
-struct RawRows {
-  uint4 d[VPT], n[VPT], r[VPT], b[VPT];
-  float rr, rb;
-};
-template <typename T, int VPT>
-__device__ __forceinline__ void load_rows(const BwdArgs& a, size_t t, int nvec, RawRows<VPT>& q) {
+// One token's gradients, for the VPT vectors of a thread: its rows (d_normed and res_out unpacked into g
+// and rhat, d_res_out and block as loaded), its sums over tokens, and what happens once every thread of
+// the block has its rows (`taken`). wg = w_post * gate of the column; the sum p of gate_t g bhat serves
+// both d_w_post (scale * gate_c * p) and d_gate_c (scale * w_post * p).
+template <typename T, int VPT, class PRE, class POST, class TAKEN>
+__device__ __forceinline__ void token_gradients(const BwdArgs& a, size_t t, int nvec, float (&g)[VPT][Row<T>::N],
+                                                float (&rhat)[VPT][Row<T>::N], const uint4 (&qd)[VPT],
+                                                const uint4 (&qb)[VPT], float rr, float rb,
+                                                float (&s_post)[VPT][Row<T>::N], float (&s_pre)[VPT][Row<T>::N],
+                                                float (*part)[32], const PRE& w_pre, const POST& wg,
+                                                const TAKEN& taken) {
+  constexpr int N = Row<T>::N;
   const size_t o = t * a.H;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const auto vec = [&](const void* p, int v) { return reinterpret_cast<const uint4*>(static_cast<const T*>(p) + o)[v]; };
+  float sum = 0.f;
+  if (a.w_pre) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float w[N];
+      w_pre(i, w);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        rhat[i][j] *= rr;
+        s_pre[i][j] = fmaf(g[i][j], rhat[i][j], s_pre[i][j]);
+        g[i][j] *= w[j];                                    // c
+        sum = fmaf(g[i][j], rhat[i][j], sum);
+      }
+    }
+    sum = block_sum(sum, part[0]) / (float)a.H;
+  } else {
+    __syncthreads();
+  }
+  taken();
+  // g: the gradient of the residual stream
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
-    const bool in = v < nvec;
-    q.n[i] = in && a.w_pre ? vec(a.d_normed, v) : zero;
-    q.r[i] = in && a.w_pre ? vec(a.res_out, v) : zero;
-    q.d[i] = in && a.d_res_out ? vec(a.d_res_out, v) : zero;
-    q.b[i] = in && a.block ? vec(a.block, v) : zero;
+    float d[N];
+    Row<T>::unpack(qd[i], d);
+#pragma unroll
+    for (int j = 0; j < N; ++j) g[i][j] = fmaf(rr, g[i][j] - rhat[i][j] * sum, d[j]);
+    if (v < nvec) reinterpret_cast<uint4*>(static_cast<T*>(a.d_residual) + o)[v] = Row<T>::pack(g[i]);
   }
-  q.rr = a.w_pre ? a.rstd_res[t] : 0.f;
-  q.rb = a.w_post ? a.rstd_block[t] : 1.f;
+  if (!a.block) {
+    __syncthreads();                                        // part[0] is free again
+    return;
+  }
+  // bhat in rhat's registers
+  const float gt = a.gate == MOE_GATE_TOKEN ? a.g[t] : 1.0f;
+  float dot = 0.f;                                          // <g wg, bhat>
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    float w[N];
+    wg(i, w);
+    Row<T>::unpack(qb[i], rhat[i]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      rhat[i][j] *= rb;
+      const float h = g[i][j] * rhat[i][j];
+      s_post[i][j] = fmaf(gt, h, s_post[i][j]);
+      dot = fmaf(h, w[j], dot);
+      g[i][j] *= w[j];
+    }
+  }
+  float mean = 0.f;
+  if (a.w_post || a.gate == MOE_GATE_TOKEN) {
+    dot = block_sum(dot, part[1]);
+    if (a.gate == MOE_GATE_TOKEN && threadIdx.x == 0) a.d_gate[t] = a.scale * dot;
+    if (a.w_post) mean = dot / (float)a.H;
+  }
+  const float f = a.scale * gt * rb;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+#pragma unroll
+    for (int j = 0; j < N; ++j) g[i][j] = f * (g[i][j] - rhat[i][j] * mean);
+    if (v < nvec) reinterpret_cast<uint4*>(static_cast<T*>(a.d_block) + o)[v] = Row<T>::pack(g[i]);
+  }
+  // part[0] may be written again: every thread has read it before the second sum's barrier
+  if (!(a.w_post || a.gate == MOE_GATE_TOKEN)) __syncthreads();
 }
 
-// MAXT: most threads of a CTA. A CTA of a wide row has an SM to itself (its sums take 24 registers per
-// 8 columns), so it loads the next token's rows before it works on the ones it has.
-template <typename T, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT) k_block_norm_bwd(const BwdArgs a) {
+// w_post * gate (per channel), each 1 where it is absent, of the vector at column c.
+template <int N>
+__device__ __forceinline__ void load_wg(const BwdArgs& a, int c, float (&w)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) w[j] = 1.0f;
+  if (a.w_post) load_param(a.w_post, c, w);
+  if (a.gate == MOE_GATE_CHANNEL) {
+    float g[N];
+    load_param(a.g, c, g);
+#pragma unroll
+    for (int j = 0; j < N; ++j) w[j] *= g[j];
+  }
+}
+
+template <typename T, int VPT>
+__device__ __forceinline__ void store_partial(const BwdArgs& a, int nvec, const float (&s_post)[VPT][Row<T>::N],
+                                              const float (&s_pre)[VPT][Row<T>::N]) {
+  constexpr int N = Row<T>::N;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v >= nvec) continue;
+    float* p = a.partial + (size_t)blockIdx.x * 2 * a.H + v * N;
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      if (a.block) *reinterpret_cast<float4*>(p + j) = make_float4(s_post[i][j], s_post[i][j + 1], s_post[i][j + 2], s_post[i][j + 3]);
+      if (a.w_pre) *reinterpret_cast<float4*>(p + a.H + j) = make_float4(s_pre[i][j], s_pre[i][j + 1], s_pre[i][j + 2], s_pre[i][j + 3]);
+    }
+  }
+}
+
+// Rows straight into registers: for rows of which two tokens' do not fit in shared memory.
+template <typename T, int VPT>
+__global__ void __launch_bounds__(1024) k_block_norm_bwd(const BwdArgs a) {
   constexpr int N = Row<T>::N;
   __shared__ float part[2][32];
   pdl_launch_dependents();
   pdl_wait();
   const int nvec = a.H / N;
-  const bool chan = a.block && a.gate == MOE_GATE_CHANNEL;
-  float sw_post[VPT][N], sw_pre[VPT][N], s_gate[VPT][N];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = 0; j < N; ++j) sw_post[i][j] = sw_pre[i][j] = s_gate[i][j] = 0.f;
-
-  RawRows<VPT> q;
-  if (blockIdx.x < (unsigned)a.T) load_rows<T, VPT>(a, blockIdx.x, nvec, q);
+  float s_post[VPT][N] = {}, s_pre[VPT][N] = {};
   for (size_t t = blockIdx.x; t < (size_t)a.T; t += gridDim.x) {
-    const size_t o = t * a.H;
     uint4 qd[VPT], qb[VPT];
-    float g[VPT][N], rhat[VPT][N], sum = 0.f;
-    const float rr = q.rr, rb = q.rb;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      Row<T>::unpack(q.n[i], g[i]);
-      Row<T>::unpack(q.r[i], rhat[i]);
-      qd[i] = q.d[i];
-      qb[i] = q.b[i];
-    }
-    if (t + gridDim.x < (size_t)a.T) load_rows<T, VPT>(a, t + gridDim.x, nvec, q);
-    if (a.w_pre) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v >= nvec) continue;
-        float w[N];
-        load_param(a.w_pre, v * N, w);
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          rhat[i][j] *= rr;
-          sw_pre[i][j] = fmaf(g[i][j], rhat[i][j], sw_pre[i][j]);
-          g[i][j] *= w[j];                                  // c
-          sum = fmaf(g[i][j], rhat[i][j], sum);
-        }
-      }
-      sum = block_sum(sum, part[0]) / (float)a.H;
-    }
-    // g: the gradient of the residual stream
+    float g[VPT][N], rhat[VPT][N];
+    const auto vec = [&](const void* p, int v) {
+      return p && v < nvec ? reinterpret_cast<const uint4*>(static_cast<const T*>(p) + t * a.H)[v] : make_uint4(0, 0, 0, 0);
+    };
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      float d[N];
-      Row<T>::unpack(qd[i], d);
-#pragma unroll
-      for (int j = 0; j < N; ++j) g[i][j] = fmaf(rr, g[i][j] - rhat[i][j] * sum, d[j]);
-      if (v < nvec) reinterpret_cast<uint4*>(static_cast<T*>(a.d_residual) + o)[v] = Row<T>::pack(g[i]);
+      Row<T>::unpack(vec(a.w_pre ? a.d_normed : nullptr, v), g[i]);
+      Row<T>::unpack(vec(a.w_pre ? a.res_out : nullptr, v), rhat[i]);
+      qd[i] = vec(a.d_res_out, v);
+      qb[i] = vec(a.block, v);
     }
-    if (!a.block) {
-      __syncthreads();                                      // part[0] is free again
-      continue;
-    }
-    // bhat in rhat's registers; c' in g's
-    const float gt = a.scale * (a.gate == MOE_GATE_TOKEN ? a.g[t] : 1.0f);
-    float dot = 0.f;                                        // <g w_post gate_c, bhat>
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      Row<T>::unpack(qb[i], rhat[i]);
-      if (v >= nvec) continue;
-      float w[N], gc[N];
-#pragma unroll
-      for (int j = 0; j < N; ++j) w[j] = gc[j] = 1.0f;
-      if (a.w_post) load_param(a.w_post, v * N, w);
-      if (chan) load_param(a.g, v * N, gc);
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float bhat = rhat[i][j] * rb;
-        rhat[i][j] = bhat;
-        if (chan) s_gate[i][j] = fmaf(g[i][j], bhat * w[j], s_gate[i][j]);
-        sw_post[i][j] = fmaf(gt * gc[j] * g[i][j], bhat, sw_post[i][j]);
-        g[i][j] *= w[j] * gc[j];
-        dot = fmaf(g[i][j], bhat, dot);
-      }
-    }
-    float mean = 0.f;
-    if (a.w_post || a.gate == MOE_GATE_TOKEN) {
-      dot = block_sum(dot, part[1]);
-      if (a.gate == MOE_GATE_TOKEN && threadIdx.x == 0) a.d_gate[t] = a.scale * dot;
-      if (a.w_post) mean = dot / (float)a.H;
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-#pragma unroll
-      for (int j = 0; j < N; ++j) g[i][j] = gt * rb * (g[i][j] - rhat[i][j] * mean);
-      if (v < nvec) reinterpret_cast<uint4*>(static_cast<T*>(a.d_block) + o)[v] = Row<T>::pack(g[i]);
-    }
-    __syncthreads();                                        // both partial arrays are free again
+    token_gradients<T, VPT>(
+        a, t, nvec, g, rhat, qd, qb, a.w_pre ? a.rstd_res[t] : 0.f, a.w_post ? a.rstd_block[t] : 1.f, s_post, s_pre, part,
+        [&](int i, float (&w)[N]) { load_param(a.w_pre, min((int)(threadIdx.x + i * blockDim.x), nvec - 1) * N, w); },
+        [&](int i, float (&w)[N]) { load_wg(a, min((int)(threadIdx.x + i * blockDim.x), nvec - 1) * N, w); }, [] {});
   }
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
-    if (v >= nvec) continue;
-    float* p = a.partial + (size_t)blockIdx.x * 3 * a.H + v * N;
-#pragma unroll
-    for (int j = 0; j < N; j += 4) {
-      if (a.w_post)
-        *reinterpret_cast<float4*>(p + j) = make_float4(sw_post[i][j], sw_post[i][j + 1], sw_post[i][j + 2], sw_post[i][j + 3]);
-      if (a.w_pre)
-        *reinterpret_cast<float4*>(p + a.H + j) = make_float4(sw_pre[i][j], sw_pre[i][j + 1], sw_pre[i][j + 2], sw_pre[i][j + 3]);
-      if (chan)
-        *reinterpret_cast<float4*>(p + 2 * a.H + j) =
-            make_float4(a.scale * s_gate[i][j], a.scale * s_gate[i][j + 1], a.scale * s_gate[i][j + 2], a.scale * s_gate[i][j + 3]);
-    }
-  }
+  store_partial<T, VPT>(a, nvec, s_post, s_pre);
 }
 
-// out[k][c] = sum over the CTAs' partial sums, for the arrays that are wanted: 32 columns per block,
-// whose 32 warps share the CTAs; each warp adds its ones in order, then the warps' sums in order.
-__global__ void __launch_bounds__(1024) k_block_norm_sum(const float* partial, int n, int H, float* w_post,
-                                                         float* w_pre, float* gate) {
+// Rows through a ring in shared memory, filled by bulk copies: a CTA of a wide row has an SM to itself
+// (its sums over tokens stay in registers), so the loads of the next tokens go on under the two block
+// reductions of this one. (Loading the next token into registers instead gained nothing: 169 us for
+// 8192 x 6144 bf16.) The ring has `depth` tokens of up to four rows.
+constexpr int kMaxDepth = 4;
+
+template <typename T, int VPT>
+__global__ void __launch_bounds__(VPT == 1 ? 768 : 1024) k_block_norm_bwd_ring(const BwdArgs a, int depth) {
+  constexpr int N = Row<T>::N;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float part[2][32];
+  __shared__ uint64_t full[kMaxDepth];
+  __shared__ int abort_flag;
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < depth; ++i) mbar_init(&full[i], 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  pdl_wait();
+  __syncthreads();
+  const int nvec = a.H / N;
+  const uint32_t row = (uint32_t)a.H * sizeof(T);
+  const auto fill = [&](int s, size_t t) {
+    const void* src[4] = {a.w_pre ? a.d_normed : nullptr, a.w_pre ? a.res_out : nullptr, a.d_res_out, a.block};
+    uint32_t n = 0;
+    for (int i = 0; i < 4; ++i) n += src[i] ? 1 : 0;
+    mbar_arrive_expect_tx(&full[s], n * row);
+    for (int i = 0; i < 4; ++i)
+      if (src[i])
+        bulk_load(ring + (size_t)(s * 4 + i) * row, static_cast<const char*>(src[i]) + t * row, row, &full[s]);
+  };
+  if (threadIdx.x == 0)
+    for (int s = 0; s < depth; ++s)
+      if (blockIdx.x + (size_t)s * gridDim.x < (size_t)a.T) fill(s, blockIdx.x + (size_t)s * gridDim.x);
+
+  // the columns' parameters stay in registers where a thread has one vector
+  float wp[VPT][N], wg[VPT][N];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = min((int)(threadIdx.x + i * blockDim.x), nvec - 1) * N;
+    if (VPT > 1) continue;
+    if (a.w_pre) load_param(a.w_pre, c, wp[i]);
+    load_wg(a, c, wg[i]);
+  }
+  float s_post[VPT][N] = {}, s_pre[VPT][N] = {};
+  int s = 0;
+  uint32_t phase = 0;
+  for (size_t t = blockIdx.x; t < (size_t)a.T; t += gridDim.x) {
+    const float rr = a.w_pre ? a.rstd_res[t] : 0.f, rb = a.w_post ? a.rstd_block[t] : 1.f;
+    // (after a wait that ran out the thread works on what there is: it has to keep up with the
+    // block's barriers)
+    mbar_wait(&full[s], phase, &abort_flag);
+    uint4 qd[VPT], qb[VPT];
+    float g[VPT][N], rhat[VPT][N];
+    const auto vec = [&](bool have, int i, int v) {
+      return have && v < nvec ? reinterpret_cast<const uint4*>(ring + (size_t)(s * 4 + i) * row)[v] : make_uint4(0, 0, 0, 0);
+    };
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      Row<T>::unpack(vec(a.w_pre, 0, v), g[i]);
+      Row<T>::unpack(vec(a.w_pre, 1, v), rhat[i]);
+      qd[i] = vec(a.d_res_out, 2, v);
+      qb[i] = vec(a.block, 3, v);
+    }
+    token_gradients<T, VPT>(
+        a, t, nvec, g, rhat, qd, qb, rr, rb, s_post, s_pre, part,
+        [&](int i, float (&w)[N]) {
+          if (VPT > 1) {
+            load_param(a.w_pre, min((int)(threadIdx.x + i * blockDim.x), nvec - 1) * N, w);
+          } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) w[j] = wp[i][j];
+          }
+        },
+        [&](int i, float (&w)[N]) {
+          if (VPT > 1) {
+            load_wg(a, min((int)(threadIdx.x + i * blockDim.x), nvec - 1) * N, w);
+          } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) w[j] = wg[i][j];
+          }
+        },
+        [&] {
+          // every thread has read its rows: the place is free
+          const size_t next = t + (size_t)depth * gridDim.x;
+          if (threadIdx.x == 0 && next < (size_t)a.T) fill(s, next);
+        });
+    if (++s == depth) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+  store_partial<T, VPT>(a, nvec, s_post, s_pre);
+  __syncthreads();
+  if (abort_flag && threadIdx.x == 0) set_status(a.status, MOE_ERR_TIMEOUT);
+}
+
+// Sums the CTAs' partial sums p (blockIdx.y 0: d_w_post = scale * gate_c * p and d_gate_c = scale *
+// w_post * p, 1: d_w_pre = p): 32 columns per block, whose 32 warps share the CTAs; each warp adds its
+// ones in order, then the warps' sums are added in order.
+struct SumArgs {
+  const float* partial;
+  int n, H;
+  float scale;
+  const float *w_post, *gate_c;      // or null: 1
+  float *d_w_post, *d_w_pre, *d_gate;
+};
+__global__ void __launch_bounds__(1024) k_block_norm_sum(const SumArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  float* out = blockIdx.y == 0 ? w_post : blockIdx.y == 1 ? w_pre : gate;
-  if (!out) return;
+  const bool pre = blockIdx.y == 1;
+  if (pre ? !a.d_w_pre : !a.d_w_post && !a.d_gate) return;
   __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < H) {
+  if (c < a.H) {
 #pragma unroll 4
-    for (int i = warp; i < n; i += 32) s += partial[((size_t)i * 3 + blockIdx.y) * H + c];
+    for (int i = warp; i < a.n; i += 32) s += a.partial[((size_t)i * 2 + blockIdx.y) * a.H + c];
   }
   part[lane][warp] = s;
   __syncthreads();
   // warp w adds up column w
   const float v = warp_sum_f(part[warp][lane]);
-  if (lane == 0 && blockIdx.x * 32 + warp < H) out[blockIdx.x * 32 + warp] = v;
+  const int col = blockIdx.x * 32 + warp;
+  if (lane != 0 || col >= a.H) return;
+  if (pre) {
+    a.d_w_pre[col] = v;
+  } else {
+    if (a.d_w_post) a.d_w_post[col] = a.scale * (a.gate_c ? a.gate_c[col] : 1.0f) * v;
+    if (a.d_gate) a.d_gate[col] = a.scale * (a.w_post ? a.w_post[col] : 1.0f) * v;
+  }
 }
 
 int check_norm(const moe_norm_t* n) {
@@ -367,14 +482,26 @@ void row_shape(int nvec, int most, int* vpt, int* threads) {
   *threads = ((nvec + *vpt - 1) / *vpt + 31) / 32 * 32;
 }
 
-// The backward's CTAs: up to 768 threads a row (the register file holds 768 with their sums), and as
-// many CTAs as make up 768 threads per SM.
-constexpr int kBwdThreads = 768;
-void bwd_shape(const moe_norm_t& n, int* vpt, int* threads, int* per_sm) {
-  row_shape(n.H / (n.dtype == MOE_BF16 ? 8 : 4), kBwdThreads, vpt, threads);
-  *per_sm = max(1, kBwdThreads / *threads);
+// The backward's CTAs. With the ring: up to 768 threads of one or two vectors (768 is what the register
+// file holds with their sums), up to 1024 of wider rows; as many CTAs as make up 768 threads per SM.
+// Without (depth 0: less than two tokens' rows fit): 1024 threads, one CTA per SM.
+struct BwdShape {
+  int vpt, threads, per_sm, depth;
+  size_t smem;
+};
+BwdShape bwd_shape(const moe_norm_t& n) {
+  BwdShape b{};
+  const size_t esz = n.dtype == MOE_BF16 ? 2 : 4, token = 4 * esz * n.H;
+  const int nvec = (int)(n.H * esz / 16);
+  row_shape(nvec, nvec <= 1536 ? 768 : 1024, &b.vpt, &b.threads);
+  b.per_sm = max(1, 768 / b.threads);
+  b.depth = (int)min((size_t)kMaxDepth, (size_t)200 * 1024 / b.per_sm / token);
+  if (b.depth < 2) b.depth = 0;
+  b.smem = b.depth * token;
+  return b;
 }
 constexpr int kMaxSms = 256;
+constexpr size_t kStatusBytes = 256;
 
 }  // namespace
 }  // namespace moe
@@ -416,9 +543,7 @@ int moe_block_norm(const moe_norm_t* n, const void* residual, const void* block,
 int moe_block_norm_workspace_size(const moe_norm_t* n, size_t* bytes) {
   MOE_TRY(check_norm(n));
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  int vpt, threads, per_sm;
-  bwd_shape(*n, &vpt, &threads, &per_sm);
-  *bytes = (size_t)max(1, min(n->T, kMaxSms * per_sm)) * 3 * n->H * sizeof(float);
+  *bytes = kStatusBytes + (size_t)max(1, min(n->T, kMaxSms * bwd_shape(*n).per_sm)) * 2 * n->H * sizeof(float);
   return MOE_OK;
 }
 
@@ -455,24 +580,30 @@ int moe_block_norm_backward(const moe_norm_t* n, const void* d_residual_out, con
   MOE_TRY(current_device_info(&dev));
   BwdArgs a{n->T, n->H, n->gate, n->scale, d_residual_out, d_normed, residual_out, block, w_post, gate, w_pre,
             rstd_block, rstd_res, d_residual, d_block, n->gate == MOE_GATE_TOKEN ? d_gate : nullptr,
-            static_cast<float*>(ws)};
+            at<float>(ws, kStatusBytes), at<int>(ws, 0)};
   const bool bf16 = n->dtype == MOE_BF16;
-  int vpt, threads, per_sm;
-  bwd_shape(*n, &vpt, &threads, &per_sm);
-#define NORM_BWD(T, MAXT)                                                            \
-  (vpt == 1 ? k_block_norm_bwd<T, 1, MAXT> : vpt == 2 ? k_block_norm_bwd<T, 2, MAXT> \
-   : vpt == 3 ? k_block_norm_bwd<T, 3, MAXT> : k_block_norm_bwd<T, 4, MAXT>)
-  void (*kern)(BwdArgs) = threads > kBwdThreads ? (bf16 ? NORM_BWD(__nv_bfloat16, 1024) : NORM_BWD(float, 1024))
-                                                : (bf16 ? NORM_BWD(__nv_bfloat16, kBwdThreads) : NORM_BWD(float, kBwdThreads));
-  const int grid = min(n->T, min(dev.sm_count, kMaxSms) * per_sm);
+  const BwdShape b = bwd_shape(*n);
+  const int grid = min(n->T, min(dev.sm_count, kMaxSms) * b.per_sm);
+#define NORM_BWD(KERN, T) (b.vpt == 1 ? KERN<T, 1> : b.vpt == 2 ? KERN<T, 2> : b.vpt == 3 ? KERN<T, 3> : KERN<T, 4>)
   if (n->T > 0) {
-    MOE_TRY(cuda_rc(launch_kernel(kern, grid, threads, 0, st, 1, a)));
+    cudaError_t e;
+    if (b.depth) {
+      auto kern = bf16 ? NORM_BWD(k_block_norm_bwd_ring, __nv_bfloat16) : NORM_BWD(k_block_norm_bwd_ring, float);
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)b.smem) != cudaSuccess)
+        return MOE_ERR_CUDA;
+      e = launch_kernel(kern, grid, b.threads, b.smem, st, 1, a, b.depth);
+    } else {
+      auto kern = bf16 ? NORM_BWD(k_block_norm_bwd, __nv_bfloat16) : NORM_BWD(k_block_norm_bwd, float);
+      e = launch_kernel(kern, grid, b.threads, 0, st, 1, a);
+    }
+    MOE_TRY(cuda_rc(e));
     count_launch();
   }
   float* chan = n->gate == MOE_GATE_CHANNEL ? d_gate : nullptr;
   if (!d_w_post && !d_w_pre && !chan) return MOE_OK;
-  const cudaError_t e = launch_kernel(k_block_norm_sum, dim3((n->H + 31) / 32, 3), 1024, 0, st, 1,
-                                      static_cast<const float*>(ws), grid, n->H, d_w_post, d_w_pre, chan);
+  const SumArgs sum{at<float>(ws, kStatusBytes), grid, n->H, n->scale, w_post,
+                    n->gate == MOE_GATE_CHANNEL ? gate : nullptr, d_w_post, d_w_pre, chan};
+  const cudaError_t e = launch_kernel(k_block_norm_sum, dim3((n->H + 31) / 32, 2), 1024, 0, st, 1, sum);
   count_launch();
   return cuda_rc(e);
 }

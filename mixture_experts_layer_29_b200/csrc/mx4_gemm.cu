@@ -323,15 +323,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int c0,
       : "memory");
 }
 
-// Untiled bulk copy global -> shared, completion counted on `bar`; 16-byte aligned both sides.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // The warp's 32 channels (one per lane) of 8 rows, v[j] of row j, turned around: afterwards v[i]
 // is channel 8 (lane / 8) + i of row lane % 8.
 __device__ __forceinline__ void turn_around(float (&v)[8], float (*stg)[kStageLd], int lane) {

@@ -95,11 +95,11 @@ def block_norm(d: Desc, residual, block, w_post, gate, w_pre, residual_out, norm
 
 
 def workspace(d: Desc, device="cuda"):
-    """Workspace of block_norm_backward (partial sums)."""
+    """Workspace of block_norm_backward (status word, partial sums), zeroed."""
     n = _SZ(0)
     abi._check(lib().moe_block_norm_workspace_size(ctypes.byref(d), ctypes.byref(n)),
                "moe_block_norm_workspace_size")
-    return torch.empty(n.value, dtype=torch.uint8, device=device)
+    return torch.zeros(n.value, dtype=torch.uint8, device=device)
 
 
 def block_norm_backward(d: Desc, d_residual_out, d_normed, residual_out, block, w_post, gate, w_pre,

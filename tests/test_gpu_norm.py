@@ -52,7 +52,7 @@ def rms(x):
     return torch.rsqrt((x * x).mean(1, keepdim=True) + EPS)
 
 
-SHAPES = [(1, 128), (3, 16), (37, 768), (5, 6144), (2, 8208), (3, 16384), (300, 1040)]
+SHAPES = [(1, 128), (3, 16), (37, 768), (5, 6144), (2, 8208), (4, 8192), (3, 16384), (300, 1040), (700, 768)]
 
 
 @pytest.mark.parametrize("T,H", SHAPES)
