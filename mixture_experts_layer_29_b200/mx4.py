@@ -70,11 +70,22 @@ def header_functions() -> list[str]:
     return sorted(set(re.findall(r"^int\s+(moe_\w+)\s*\(", open(HEADER).read(), flags=re.M)))
 
 
-def _call(name: str, *args):
-    abi._check(getattr(lib(), name)(*args), name)
+# the current device and its current stream, without the objects around them: a call at a decode
+# step takes the GPU a few microseconds, and torch.cuda's own functions as much again
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _tensor(t, name, dtypes, shape=None, device=None, optional=False, contiguous=True):
+def _stream(stream, dev: int) -> int:
+    return _raw_stream(dev) if stream is None else abi._stream(stream)
+
+
+def _check(rc: int, where: str):
+    if rc != 0:
+        raise abi.MoEError(rc, where)
+
+
+def _tensor(t, name, dtypes, shape=None, optional=False, contiguous=True, dev=None):
     """Checks one tensor argument and returns its address (None for an absent optional one)."""
     if t is None and optional:
         return None
@@ -82,13 +93,12 @@ def _tensor(t, name, dtypes, shape=None, device=None, optional=False, contiguous
         raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    if t.get_device() != (_device() if dev is None else dev) or not t.is_cuda:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{_device()}")
     return t.data_ptr()
 
 
@@ -96,42 +106,43 @@ class Matrix:
     """A 4-bit matrix: rows of K elements in groups (see include/moe_mx4.h for the layout).
 
     codes [rows, K / 2] uint8, scales uint8, offsets int32 [groups + 1] (ragged groups) or None
-    (groups of rows / groups rows each), tensor_scale fp32 [1] or [groups] (nvfp4) or None."""
+    (groups of rows / groups rows each), tensor_scale fp32 [1] or [groups] (nvfp4) or None. The
+    buffers are checked and kept when the matrix is made; their contents may change."""
 
-    def __init__(self, fmt, rows, K, groups=1, offsets=None, tensor_scale=None, codes=None,
-                 scales=None, device="cuda"):
+    def __init__(self, fmt, rows, K, groups=1, offsets=None, tensor_scale=None, codes=None, device="cuda"):
         if fmt not in FORMATS:
             raise ValueError(f"format {fmt!r}: one of {sorted(FORMATS)}")
         if offsets is None and groups > 0 and rows % groups != 0:
             raise ValueError(f"{rows} rows in {groups} equal groups: give offsets")
         if tensor_scale is not None and tensor_scale.numel() not in (1, groups):
             raise ValueError(f"tensor_scale: {tensor_scale.numel()} values, expected 1 or {groups}")
-        self.fmt, self.rows, self.K, self.groups = fmt, rows, K, groups
-        self.offsets, self.tensor_scale = offsets, tensor_scale
-        d = self._sizes()
+        self._d = d = Desc(FORMATS[fmt], rows, K, groups, 0 if offsets is not None else rows // max(groups, 1),
+                           int(tensor_scale is not None and tensor_scale.numel() > 1), None, None, None, None)
         n = _SZ(0)
-        _call("moe_mx4_scale_bytes", ctypes.byref(d), ctypes.byref(n))
-        self.codes = torch.empty(rows, K // 2, dtype=torch.uint8, device=device) if codes is None else codes
-        self.scales = torch.empty(n.value, dtype=torch.uint8, device=device) if scales is None else scales
-        if self.scales.numel() < n.value:
-            raise ValueError(f"scales: {self.scales.numel()} bytes, expected {n.value}")
+        _check(lib().moe_mx4_scale_bytes(ctypes.byref(d), ctypes.byref(n)), "moe_mx4_scale_bytes")
+        codes = torch.empty(rows, K // 2, dtype=torch.uint8, device=device) if codes is None else codes
+        scales = torch.empty(n.value, dtype=torch.uint8, device=device)
+        self._parts = (fmt, rows, K, groups, offsets, tensor_scale, codes.view(rows, K // 2), scales)
+        d.offsets = _tensor(offsets, "offsets", (torch.int32,), (groups + 1,), optional=True)
+        d.factor = _tensor(tensor_scale, "tensor_scale", (torch.float32,), optional=True)
+        d.codes = _tensor(codes, "codes", (torch.uint8,))
+        d.scales = _tensor(scales, "scales", (torch.uint8,))
+        self._dev = codes.get_device()
 
-    def _sizes(self) -> Desc:
-        ts = self.tensor_scale
-        return Desc(FORMATS[self.fmt], self.rows, self.K, self.groups,
-                    0 if self.offsets is not None else self.rows // max(self.groups, 1),
-                    int(ts is not None and ts.numel() > 1), None, None, None, None)
+    fmt = property(lambda self: self._parts[0])
+    rows = property(lambda self: self._parts[1])
+    K = property(lambda self: self._parts[2])
+    groups = property(lambda self: self._parts[3])
+    offsets = property(lambda self: self._parts[4])
+    tensor_scale = property(lambda self: self._parts[5])
+    codes = property(lambda self: self._parts[6])
+    scales = property(lambda self: self._parts[7])
 
-    def desc(self) -> Desc:
-        """The matrix as the C ABI takes it; checks the buffers."""
-        d = self._sizes()
-        d.offsets = _tensor(self.offsets, "offsets", (torch.int32,), (self.groups + 1,), optional=True)
-        d.factor = _tensor(self.tensor_scale, "tensor_scale", (torch.float32,), optional=True)
-        d.codes = _tensor(self.codes, "codes", (torch.uint8,))
-        if self.codes.numel() != self.rows * (self.K // 2):
-            raise ValueError(f"codes: {self.codes.numel()} bytes, expected {self.rows * (self.K // 2)}")
-        d.scales = _tensor(self.scales, "scales", (torch.uint8,))
-        return d
+    def desc(self, dev: int):
+        """The matrix as the C ABI takes it, for a call on device `dev`."""
+        if self._dev != dev:
+            raise ValueError(f"a 4-bit matrix on cuda:{self._dev}, but the current device is cuda:{dev}")
+        return ctypes.byref(self._d)
 
 
 def allocate(fmt, rows, K, groups=1, offsets=None, tensor_scale=None, device="cuda") -> Matrix:
@@ -146,7 +157,8 @@ def from_checkpoint(fmt, codes, scales, tensor_scale=None, stream=None) -> Matri
     groups, N, half = codes.shape
     m = Matrix(fmt, groups * N, 2 * half, groups, None, tensor_scale, codes=codes, device=codes.device)
     p = _tensor(scales, "scales", (torch.uint8,), (groups, N, m.K // BLOCK[fmt]))
-    _call("moe_mx4_pack_scales", ctypes.byref(m.desc()), p, abi._stream(stream))
+    dev = _device()
+    _check(lib().moe_mx4_pack_scales(m.desc(dev), p, _stream(stream, dev)), "moe_mx4_pack_scales")
     return m
 
 
@@ -157,13 +169,16 @@ def quantize_weight(w, fmt, tensor_scale=None, stream=None) -> Matrix:
     return quantize(w.reshape(groups * N, K), m, stream=stream)
 
 
-def _rows(t, name, m, rows):
+_FLOATS = (torch.bfloat16, torch.float32)
+_F32, _I32T, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
+
+
+def _rows(t, name, K, rows, dev):
     """(address, dtype code, row stride) of a [rows, K] operand whose rows may be strided."""
-    p = _tensor(t, name, tuple(_DTYPES), (rows, m.K), contiguous=False)
-    if rows and m.K > 1 and t.stride(1) != 1:
+    p = _tensor(t, name, _FLOATS, (rows, K), contiguous=False, dev=dev)
+    if rows and t.stride(1) != 1:
         raise ValueError(f"{name}: elements of a row are not adjacent")
-    ld = t.stride(0) if rows > 1 else m.K
-    return p, _DTYPES[t.dtype], ld
+    return p, _DTYPES[t.dtype], t.stride(0) if rows > 1 else K
 
 
 def quantize(x, m: Matrix, row_of=None, status=None, stream=None) -> Matrix:
@@ -171,44 +186,51 @@ def quantize(x, m: Matrix, row_of=None, status=None, stream=None) -> Matrix:
     [tokens, picks] (abi.permute's), row t of x [tokens, K] goes to each row row_of[t, p] >= 0
     of m. status: a device int32 that receives a device-side check's failure (a workspace's
     first word, for abi.read_device_status)."""
+    dev = _device()
     tokens, picks = m.rows, 0
     if row_of is not None:
         if row_of.dim() != 2:
             raise ValueError("row_of: [tokens, picks]")
         tokens, picks = row_of.shape
-    p, dt, ld = _rows(x, "x", m, tokens)
-    _call("moe_mx4_quantize", ctypes.byref(m.desc()), p, dt, ld,
-          _tensor(row_of, "row_of", (torch.int32,), optional=True), tokens, picks,
-          None if status is None else status.data_ptr(), abi._stream(stream))
+        row_of = _tensor(row_of, "row_of", _I32T, dev=dev)
+    p, dt, ld = _rows(x, "x", m.K, tokens, dev)
+    if status is not None:
+        status = _tensor(status, "status", (torch.uint8, torch.int32), dev=dev)
+    _check(lib().moe_mx4_quantize(m.desc(dev), p, dt, ld, row_of, tokens, picks, status, _stream(stream, dev)),
+           "moe_mx4_quantize")
     return m
 
 
 def dequantize(m: Matrix, out, stream=None):
     """The values of m into out [rows, K] bf16 or fp32 (rows of no group are left alone)."""
-    p, dt, ld = _rows(out, "out", m, m.rows)
-    _call("moe_mx4_dequantize", ctypes.byref(m.desc()), p, dt, ld, abi._stream(stream))
+    dev = _device()
+    p, dt, ld = _rows(out, "out", m.K, m.rows, dev)
+    _check(lib().moe_mx4_dequantize(m.desc(dev), p, dt, ld, _stream(stream, dev)), "moe_mx4_dequantize")
     return out
 
 
 def gemm_workspace(device="cuda"):
+    """Workspace of grouped_gemm (status word), zeroed."""
     n = _SZ(0)
-    _call("moe_mx4_gemm_workspace_size", ctypes.byref(n))
+    _check(lib().moe_mx4_gemm_workspace_size(ctypes.byref(n)), "moe_mx4_gemm_workspace_size")
     return torch.zeros(n.value, dtype=torch.uint8, device=device)
 
 
 def grouped_gemm(a: Matrix, w: Matrix, out, ws, stream=None):
     """out[r] = a[r] . w[g]^T for the rows r of each group g; out [a.rows, N] bf16 or fp32."""
-    p = _tensor(out, "out", tuple(_DTYPES), (a.rows, w.rows // max(w.groups, 1)))
-    _call("moe_mx4_grouped_gemm", ctypes.byref(a.desc()), ctypes.byref(w.desc()), p,
-          _DTYPES[out.dtype], _tensor(ws, "ws", (torch.uint8,)), ws.numel(), abi._stream(stream))
+    dev = _device()
+    p = _tensor(out, "out", _FLOATS, (a.rows, w.rows // max(w.groups, 1)), dev=dev)
+    _check(lib().moe_mx4_grouped_gemm(a.desc(dev), w.desc(dev), p, _DTYPES[out.dtype],
+                                      _tensor(ws, "ws", _U8, dev=dev), ws.numel(), _stream(stream, dev)),
+           "moe_mx4_grouped_gemm")
     return out
 
 
 def ffn_workspace(a: Matrix, w_gate_up: Matrix, device="cuda"):
     """Workspace of grouped_ffn (status word and h), zeroed."""
     n = _SZ(0)
-    _call("moe_mx4_ffn_workspace_size", ctypes.byref(a.desc()), ctypes.byref(w_gate_up.desc()),
-          ctypes.byref(n))
+    _check(lib().moe_mx4_ffn_workspace_size(ctypes.byref(a._d), ctypes.byref(w_gate_up._d), ctypes.byref(n)),
+           "moe_mx4_ffn_workspace_size")
     return torch.zeros(n.value, dtype=torch.uint8, device=device)
 
 
@@ -217,14 +239,13 @@ def grouped_ffn(a: Matrix, w_gate_up: Matrix, w_down: Matrix, out, ws, h_scale=N
     """The grouped SwiGLU FFN on 4-bit experts. Without perm_token: out [a.rows, H] bf16 or
     fp32, one row each. With it (fused combine): out fp32 [tokens, H], to which
     scale * row_gate[r] * y[r] is added at perm_token[r]."""
-    shape = (a.rows, a.K) if perm_token is None else (out.shape[0], a.K)
-    p = _tensor(out, "out", tuple(_DTYPES), shape)
-    one = (torch.float32,)
-    _call("moe_mx4_grouped_ffn", ctypes.byref(a.desc()), ctypes.byref(w_gate_up.desc()),
-          ctypes.byref(w_down.desc()), _tensor(h_scale, "h_scale", one, (1,), optional=True),
-          _tensor(perm_token, "perm_token", (torch.int32,), optional=True),
-          _tensor(row_gate, "row_gate", one, optional=True), float(scale), p, _DTYPES[out.dtype],
-          _tensor(ws, "ws", (torch.uint8,)), ws.numel(), abi._stream(stream))
+    dev = _device()
+    p = _tensor(out, "out", _FLOATS, (a.rows if perm_token is None else out.shape[0], a.K), dev=dev)
+    _check(lib().moe_mx4_grouped_ffn(
+        a.desc(dev), w_gate_up.desc(dev), w_down.desc(dev), _tensor(h_scale, "h_scale", _F32, (1,), True, dev=dev),
+        _tensor(perm_token, "perm_token", _I32T, None, True, dev=dev),
+        _tensor(row_gate, "row_gate", _F32, None, True, dev=dev), scale, p, _DTYPES[out.dtype],
+        _tensor(ws, "ws", _U8, dev=dev), ws.numel(), _stream(stream, dev)), "moe_mx4_grouped_ffn")
     return out
 
 

@@ -20,7 +20,7 @@ import re
 import torch
 
 from . import abi
-from .mx4 import _tensor
+from .mx4 import _F32, _U8, _check, _device, _stream, _tensor
 
 HEADER = os.path.join(os.path.dirname(abi.HEADER), "moe_norm.h")
 GATES = {"none": 0, "token": 1, "channel": 2}
@@ -66,39 +66,32 @@ def make_desc(T, H, dtype="bf16", gate="none", eps=1e-5, scale=1.0) -> Desc:
     return Desc(T, H, dt, GATES[gate], eps, scale)
 
 
-def _checker(d: Desc):
-    dt = (torch.bfloat16,) if d.dtype == abi.MOE_BF16 else (torch.float32,)
-    f32 = (torch.float32,)
+_ROWS = {abi.MOE_BF16: (torch.bfloat16,), abi.MOE_FP32: (torch.float32,)}
 
-    def rows(t, name, optional=True):
-        return _tensor(t, name, dt, (d.T, d.H), optional=optional)
 
-    def chan(t, name):
-        return _tensor(t, name, f32, (d.H,), optional=True)
-
-    def tok(t, name):
-        return _tensor(t, name, f32, (d.T,), optional=True)
-
-    return rows, chan, tok, (tok if d.gate == GATES["token"] else chan)
+def _of_gate(d: Desc):
+    return (d.T,) if d.gate == GATES["token"] else (d.H,)
 
 
 def block_norm(d: Desc, residual, block, w_post, gate, w_pre, residual_out, normed, rstd_block=None,
                rstd_res=None, stream=None):
     """moe_block_norm; returns (residual_out, normed)."""
-    rows, chan, tok, of_gate = _checker(d)
-    abi._check(lib().moe_block_norm(
-        ctypes.byref(d), rows(residual, "residual", False), rows(block, "block"), chan(w_post, "w_post"),
-        of_gate(gate, "gate"), chan(w_pre, "w_pre"), rows(residual_out, "residual_out"),
-        rows(normed, "normed"), tok(rstd_block, "rstd_block"), tok(rstd_res, "rstd_res"),
-        abi._stream(stream)), "moe_block_norm")
+    dev, rows, dt, T, H = _device(), (d.T, d.H), _ROWS.get(d.dtype, ()), (d.T,), (d.H,)
+    _check(lib().moe_block_norm(
+        ctypes.byref(d), _tensor(residual, "residual", dt, rows, dev=dev),
+        _tensor(block, "block", dt, rows, True, dev=dev), _tensor(w_post, "w_post", _F32, H, True, dev=dev),
+        _tensor(gate, "gate", _F32, _of_gate(d), True, dev=dev), _tensor(w_pre, "w_pre", _F32, H, True, dev=dev),
+        _tensor(residual_out, "residual_out", dt, rows, True, dev=dev),
+        _tensor(normed, "normed", dt, rows, True, dev=dev),
+        _tensor(rstd_block, "rstd_block", _F32, T, True, dev=dev),
+        _tensor(rstd_res, "rstd_res", _F32, T, True, dev=dev), _stream(stream, dev)), "moe_block_norm")
     return residual_out, normed
 
 
 def workspace(d: Desc, device="cuda"):
     """Workspace of block_norm_backward (status word, partial sums), zeroed."""
     n = _SZ(0)
-    abi._check(lib().moe_block_norm_workspace_size(ctypes.byref(d), ctypes.byref(n)),
-               "moe_block_norm_workspace_size")
+    _check(lib().moe_block_norm_workspace_size(ctypes.byref(d), ctypes.byref(n)), "moe_block_norm_workspace_size")
     return torch.zeros(n.value, dtype=torch.uint8, device=device)
 
 
@@ -106,14 +99,19 @@ def block_norm_backward(d: Desc, d_residual_out, d_normed, residual_out, block, 
                         rstd_block, rstd_res, d_residual, d_block, d_w_post, d_gate, d_w_pre, ws,
                         stream=None):
     """moe_block_norm_backward: writes the gradients of the parts that the forward had."""
-    rows, chan, tok, of_gate = _checker(d)
-    abi._check(lib().moe_block_norm_backward(
-        ctypes.byref(d), rows(d_residual_out, "d_residual_out"), rows(d_normed, "d_normed"),
-        rows(residual_out, "residual_out"), rows(block, "block"), chan(w_post, "w_post"),
-        of_gate(gate, "gate"), chan(w_pre, "w_pre"), tok(rstd_block, "rstd_block"),
-        tok(rstd_res, "rstd_res"), rows(d_residual, "d_residual", False), rows(d_block, "d_block"),
-        chan(d_w_post, "d_w_post"), of_gate(d_gate, "d_gate"), chan(d_w_pre, "d_w_pre"),
-        _tensor(ws, "ws", (torch.uint8,)), ws.numel(), abi._stream(stream)), "moe_block_norm_backward")
+    dev, rows, dt, T, H, G = _device(), (d.T, d.H), _ROWS.get(d.dtype, ()), (d.T,), (d.H,), _of_gate(d)
+
+    def opt(t, name, dtypes, shape):
+        return _tensor(t, name, dtypes, shape, True, dev=dev)
+
+    _check(lib().moe_block_norm_backward(
+        ctypes.byref(d), opt(d_residual_out, "d_residual_out", dt, rows), opt(d_normed, "d_normed", dt, rows),
+        opt(residual_out, "residual_out", dt, rows), opt(block, "block", dt, rows), opt(w_post, "w_post", _F32, H),
+        opt(gate, "gate", _F32, G), opt(w_pre, "w_pre", _F32, H), opt(rstd_block, "rstd_block", _F32, T),
+        opt(rstd_res, "rstd_res", _F32, T), _tensor(d_residual, "d_residual", dt, rows, dev=dev),
+        opt(d_block, "d_block", dt, rows), opt(d_w_post, "d_w_post", _F32, H), opt(d_gate, "d_gate", _F32, G),
+        opt(d_w_pre, "d_w_pre", _F32, H), _tensor(ws, "ws", _U8, dev=dev), ws.numel(), _stream(stream, dev)),
+        "moe_block_norm_backward")
 
 
 class MoEBlock:
