@@ -13,14 +13,16 @@
  *                  holds an infinity or a NaN gets b = 255, and all its values are NaN.
  *   MOE_MX4_NVFP4  blocks of 16, scale byte e4m3: s = e4m3(|x| / (6 t)) (at most 448), element
  *                  e2m1(x / (s t)), value element * s * t, with t the tensor's fp32 factor
- *                  (1 when no factor is given). A block with s = 0 is all zeros. A block with
+ *                  (1 when no factor is given; positive, from 2^-100 to 2^100). A block with s = 0 is all zeros. A block with
  *                  an infinity or a NaN gets the e4m3 NaN, and all its values are NaN.
  * The fp32 operations round to nearest: 6 t, |x| / (6 t), s t and x / (s t), one each.
  *
  * Rows and groups. A 4-bit matrix has `rows` rows of K elements in `groups` groups, group g
  * the rows [o_g, o_{g+1}):
  *   ragged   o = `offsets`, device int32 [groups + 1], ascending from 0, o_groups <= rows.
- *            Rows from o_groups on belong to no group: no call reads or writes them.
+ *            Rows from o_groups on belong to no group: no call writes them, and what they hold
+ *            has no effect. (The products report offsets that are not so as
+ *            MOE_ERR_DEVICE_CHECK and keep to the buffers; their outputs are then undefined.)
  *   uniform  `offsets` NULL: o_g = g * group_rows, groups * group_rows == rows.
  *
  * Layout. codes: [rows, K / 2] bytes, the even element of a pair in the low half. scales: the
@@ -32,7 +34,7 @@
  * partly filled 128 rows whatever the offsets are; moe_mx4_scale_bytes gives the buffer's
  * size. Scale bytes of rows that a group does not have are never used.
  *
- * Limits: K >= 128 and a multiple of 128, 1 <= groups <= 1024, 0 <= rows < 2^31,
+ * Limits: K >= 128 and a multiple of 128, 1 <= groups <= 1024, 0 <= rows < 2^31 - 1025,
  * rows * K < 2^46. Other sizes give MOE_ERR_UNSUPPORTED (negative ones and a group_rows that
  * does not match MOE_ERR_INVALID_ARG). rows = 0 checks the arguments and launches nothing.
  */

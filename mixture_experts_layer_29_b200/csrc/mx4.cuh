@@ -56,7 +56,7 @@ __device__ __forceinline__ int mx4_find_group(const Mx4Rows& m, int r, int& o_g)
   if (!le) return -1;
   const int g = lo + 31 - __clz(le);
   if (g >= m.groups) return -1;
-  o_g = m.offsets[g];
+  o_g = max(m.offsets[g], 0);
   return g;
 }
 

@@ -418,17 +418,26 @@ __device__ __forceinline__ void epi_store(const Args& a, const Tile& t, int c, i
   }
 }
 
-// The tables of the groups' rows and row tiles, by every thread of the CTA.
+// The tables of the groups' rows and row tiles, by every thread of the CTA. Offsets outside the matrix
+// (or, below, out of order) leave no row outside of it: they are clamped and reported.
 template <class S>
 __device__ __forceinline__ void build_table(S& s, const Args& g, int NT) {
-  for (int i = threadIdx.x; i <= g.a.groups; i += blockDim.x) s.offs[i] = g.a.begin(i);
+  for (int i = threadIdx.x; i <= g.a.groups; i += blockDim.x) {
+    const int o = g.a.begin(i), c = min(max(o, 0), g.a.rows);
+    if (o != c || (i == 0 && o != 0)) set_status(g.status, MOE_ERR_DEVICE_CHECK);
+    s.offs[i] = c;
+  }
   __syncthreads();
   if (threadIdx.x >= 64 && threadIdx.x < 96) {
     // toff[e] = sum over e' < e of ceil(count_e' / NT)
     const int lane = threadIdx.x & 31;
     const int per = (g.a.groups + 31) / 32;
     const int b = lane * per;
-    auto tiles_of = [&](int e) { return (s.offs[e + 1] - s.offs[e] + NT - 1) / NT; };
+    auto tiles_of = [&](int e) {
+      const int n = s.offs[e + 1] - s.offs[e];
+      if (n < 0) set_status(g.status, MOE_ERR_DEVICE_CHECK);
+      return n > 0 ? (n + NT - 1) / NT : 0;
+    };
     int local = 0;
     for (int i = 0; i < per; ++i)
       if (b + i < g.a.groups) local += tiles_of(b + i);

@@ -242,7 +242,8 @@ int mx4_check(const moe_mx4_t* m) {
   if (m->rows < 0 || m->K <= 0 || m->groups <= 0 || m->group_rows < 0) return MOE_ERR_INVALID_ARG;
   if (m->factor_per_group != 0 && m->factor_per_group != 1) return MOE_ERR_INVALID_ARG;
   if (m->groups > kMx4MaxGroups || m->K % 128 != 0) return MOE_ERR_UNSUPPORTED;
-  if ((int64_t)m->rows * m->K >= (1ll << 46)) return MOE_ERR_UNSUPPORTED;
+  // (the last tile's coordinates may run on by a tile)
+  if (m->rows >= INT32_MAX - 1024 || (int64_t)m->rows * m->K >= (1ll << 46)) return MOE_ERR_UNSUPPORTED;
   if (m->offsets) {
     if (m->group_rows != 0) return MOE_ERR_INVALID_ARG;
     if (!aligned16(m->offsets)) return MOE_ERR_ALIGNMENT;

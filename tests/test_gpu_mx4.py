@@ -157,12 +157,12 @@ def small_checkpoint(shape, fmt, seed):
     return code, byte, v
 
 
-COUNTS = [[1], [16], [0, 0, 3], [64, 65, 1], [17, 0, 130, 63], [193, 0, 192, 191], [400, 1]]
+COUNTS = [[1], [16], [0, 0, 3], [0, 0], [64, 65, 1], [17, 0, 130, 63], [193, 0, 192, 191], [400, 1]]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("counts", COUNTS)
-@pytest.mark.parametrize("N,K", [(128, 128), (256, 256), (200, 384), (515, 640)])
+@pytest.mark.parametrize("N,K", [(1, 128), (128, 128), (256, 256), (200, 384), (515, 640)])
 def test_product_of_small_numbers_is_exact(cuda_device, fmt, counts, N, K):
     """|products| <= 144 in steps of 1/16, so sums of 640 are exact in fp32 in any order: a
     wrong scale, row, column or accumulator shows as a difference."""
@@ -182,6 +182,38 @@ def test_product_of_small_numbers_is_exact(cuda_device, fmt, counts, N, K):
     assert abi.read_device_status(ws) == 0
     assert torch.equal(out[:rows].double(), y)
     assert (out[rows:] == 3.0).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("counts,N", [([3000, 1, 2500, 190], 2056), ([64, 1, 7, 0, 65, 63] * 10, 4104)])
+def test_many_tiles_per_cta_are_exact(cuda_device, fmt, counts, N):
+    """More tiles than a persistent CTA (or pair) takes in one turn: 31 and 17 row and channel tiles,
+    and 70 x 17; K = 512 in two stages."""
+    K, groups, off = 512, len(counts), offsets_of(counts)
+    code, byte, a = small_checkpoint((off[-1], K), fmt, 5)
+    wc, wb, w = small_checkpoint((groups, N, K), fmt, 6)
+    m = mx4.allocate(fmt, off[-1], K, groups, dev(off))
+    m.codes.copy_(ref.pack(code))
+    m.scales[ref.scale_index(off, K, fmt, "cuda")] = byte
+    ws = mx4.gemm_workspace()
+    y, _ = ref.grouped(a, w, off)
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.empty(off[-1], N, device="cuda", dtype=dtype)
+        mx4.grouped_gemm(m, mx4.from_checkpoint(fmt, ref.pack(wc), wb), out, ws)
+        assert torch.equal(out, y.to(dtype))
+    assert abi.read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("bad", [[0, 40, 30, 70], [0, 40, 50, 90], [5, 40, 50, 70]])
+def test_products_report_offsets_outside_the_matrix(cuda_device, fmt, bad):
+    a = mx4.allocate(fmt, 70, 256, 3, dev(bad))
+    a.codes.zero_()
+    a.scales.zero_()
+    w = mx4.quantize_weight(torch.zeros(3, 128, 256, device="cuda"), fmt)
+    ws = mx4.gemm_workspace()
+    mx4.grouped_gemm(a, w, torch.empty(70, 128, device="cuda"), ws)
+    assert abi.read_device_status(ws) == -6 and abi.read_device_status(ws) == 0
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
