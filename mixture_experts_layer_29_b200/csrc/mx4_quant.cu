@@ -92,12 +92,17 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const QuantArgs 
       for (int i = 0; i < 8; ++i) v[s][i] = 0.f;
     }
   }
-  int g = -1, o_g = 0, row = -1;
-  if (!q.row_of) {      // one destination: its group is looked for while the loads are under way
-    row = t;
+  // its group, looked for while the loads are under way: of the row, or of lane p's pick
+  int g, o_g = 0, row = t;
+  if (q.row_of) {
+    g = mx4_find_groups(q.m, dst, o_g);
+    if (dst >= 0 && g < 0) set_status(q.status, MOE_ERR_DEVICE_CHECK);
+    left = __ballot_sync(0xffffffffu, g >= 0);
+  } else {
     g = mx4_find_group(q.m, row, o_g);
     if (g < 0) return;
   }
+  const int my_g = g, my_o = o_g;
   const Mx4Factor f = mx4_factor(NV && q.factor ? q.factor[q.factor_per_group ? g : 0] : 1.0f);
 
   uint32_t code[S], scale[S];
@@ -123,11 +128,8 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const QuantArgs 
     left &= left - 1;
     if (q.row_of) {
       row = __shfl_sync(0xffffffffu, dst, p);
-      g = mx4_find_group(q.m, row, o_g);
-      if (g < 0) {
-        if (lane == 0) set_status(q.status, MOE_ERR_DEVICE_CHECK);
-        continue;
-      }
+      g = __shfl_sync(0xffffffffu, my_g, p);
+      o_g = __shfl_sync(0xffffffffu, my_o, p);
     }
     uint8_t* codes = q.codes + (int64_t)row * (q.m.K / 2);
     constexpr int kPiece = mx4_block(NV) / 2;     // lanes of a piece's row: 4 blocks of 8-element lanes
