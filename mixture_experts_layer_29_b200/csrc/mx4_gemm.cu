@@ -132,7 +132,9 @@ struct Pair {
   static constexpr int SLOTS = FIT < STAGES ? FIT : STAGES;
   static_assert(STAGE % 1024 == 0, "128-byte-swizzled boxes need 1024-byte alignment");
   static_assert(SLOTS >= 3, "TMEM budget");
-  static_assert(STAGES % 2 == 0 && SF_STAGES % 2 == 0, "the two sets of scale warps keep their own stages");
+  // each of the two sets of scale warps keeps to its own stages of this ring, so that it sees every
+  // phase of their barriers (one that misses a phase takes the phase before for the one it waits for)
+  static_assert(SF_STAGES % 2 == 0, "a stage of scales belongs to one set of warps");
 };
 
 template <class C>
@@ -993,7 +995,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         // like the accumulators, TMEM columns are handed over by the tcgen05 fences
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.full[ostage]), 0));
-        ostage = ostage + 2 < STAGES ? ostage + 2 : set;
+        ostage += 2;
+        if (ostage >= STAGES) ostage -= STAGES;
         sl += 2;
         if (sl >= C::SLOTS) sl -= C::SLOTS;
         before += 2;
