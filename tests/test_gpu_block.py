@@ -236,3 +236,68 @@ def test_python_refuses_wrong_tensors(cuda_device):
         mx4.Mx4MoELayer(abi.make_shape(8, 256, 128, 12, 4, 3, "fp32"), None, None, None, None)
     with pytest.raises(ValueError, match="w_gate_up"):
         mx4.Mx4MoELayer(abi.shape_of(cfg), None, None, w, w)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("counts,H,I", [([1500, 3, 0, 2200, 700, 1100], 1536, 1024), ([40, 64, 1, 0, 13, 30] * 8, 1536, 1024)])
+def test_calls_back_to_back_agree(cuda_device, fmt, counts, H, I):
+    """Launches that overlap their predecessors' ends, with nothing between them: every one gives the
+    first one's bits, captured and not. Six and four stages per tile, more tiles than CTAs."""
+    groups = len(counts)
+    off = [0]
+    for c in counts:
+        off.append(off[-1] + c)
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn(off[-1], H, device="cuda", generator=g).to(torch.bfloat16)
+    wgu = mx4.quantize_weight(torch.randn(groups, 2 * I, H, device="cuda", generator=g) * 0.05, fmt)
+    wd = mx4.quantize_weight(torch.randn(groups, H, I, device="cuda", generator=g) * 0.05, fmt)
+    a = mx4.allocate(fmt, off[-1], H, groups, o)
+    ws, wg = mx4.ffn_workspace(a, wgu), mx4.gemm_workspace()
+    first = torch.empty(off[-1], H, dtype=torch.bfloat16, device="cuda")
+    gu = torch.empty(off[-1], 2 * I, dtype=torch.bfloat16, device="cuda")
+    mx4.quantize(x, a)
+    mx4.grouped_ffn(a, wgu, wd, first, ws)
+    mx4.grouped_gemm(a, wgu, gu, wg)
+    torch.cuda.synchronize()
+    outs = [torch.zeros_like(first) for _ in range(24)]
+    gus = [torch.zeros_like(gu) for _ in range(8)]
+
+    def step():
+        for i, out in enumerate(outs):
+            if i % 3 == 0:
+                mx4.quantize(x, a)
+            mx4.grouped_ffn(a, wgu, wd, out, ws)
+        for out in gus:
+            mx4.grouped_gemm(a, wgu, out, wg)
+
+    step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, first) for out in outs) and all(torch.equal(out, gu) for out in gus)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for out in outs + gus:
+        out.zero_()
+    for _ in range(4):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, first) for out in outs) and all(torch.equal(out, gu) for out in gus)
+    assert abi.read_device_status(ws) == 0 and abi.read_device_status(wg) == 0
+
+
+@pytest.mark.parametrize("T,H,dtype", [(900, 6144, "bf16"), (2000, 768, "fp32"), (700, 8192, "fp32")])
+def test_norm_gradients_back_to_back_agree(cuda_device, T, H, dtype):
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    d = norm.make_desc(T, H, dtype, "token", 1e-5, 0.5)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rows = lambda: torch.randn(T, H, device="cuda", generator=g).to(dt)     # noqa: E731
+    vec = lambda n: torch.rand(n, device="cuda", generator=g) + 0.5        # noqa: E731
+    args = [rows(), rows(), rows(), rows(), vec(H), vec(T), vec(H), vec(T), vec(T)]
+    outs = [[torch.zeros_like(args[0]), torch.zeros_like(args[0]), vec(H), vec(T), vec(H)] for _ in range(20)]
+    ws = norm.workspace(d)
+    for o in outs:
+        norm.block_norm_backward(d, *args, *o, ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for o in outs for u, v in zip(o, outs[0]))
+    assert abi.read_device_status(ws) == 0
