@@ -419,9 +419,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 768 : 1024) k_block_norm_bwd_ring(c
             for (int j = 0; j < N; ++j) w[j] = wg[i][j];
           }
         });
-    // every thread has read its rows (there was a barrier since): the place is free. Filling it at the
-    // end of the token rather than at that barrier keeps the copies' issue, some 140 cycles each, out
-    // of the block's way (115 us instead of 132 for 8192 x 6144 bf16)
+    // every thread has used its rows before the token's last barrier (loads that are only under way
+    // there would not do): the place is free. Filling it at the end of the token keeps the copies'
+    // issue, some 140 cycles each, out of the block's way (115 us instead of 132 for 8192 x 6144 bf16)
     const size_t next = t + (size_t)depth * gridDim.x;
     if (threadIdx.x == 0 && next < (size_t)a.T) fill(s, next);
     if (++s == depth) {

@@ -289,7 +289,8 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// mbar_wait by every lane of the warp, the same answer in each.
+// mbar_wait by every lane of the warp, the same answer in each: lanes that go on to read what the
+// barrier guards have to wait themselves, a value shuffled from one that did orders no memory.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
@@ -612,11 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = decode(s, g, tile, NT);
       const int upper = ((t.row0 - t.o_g) & 64) / 8;         // the rows' half of their scale tile
       for (int kb = 0; kb < g.kstages; ++kb) {
-        // one lane waits, the warp follows it
-        int w_ok = 1;
-        if (lane == 0) w_ok = mbar_wait(&s.full[stage], phase, abort_flag) ? 1 : 0;
-        w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
-        if (!w_ok) { ok = false; break; }
+        ok = warp_wait(&s.full[stage], phase, abort_flag);
+        if (!ok) break;
         tc_fence_after();
         const uint8_t* sf = s.ring[stage] + 2 * W_BYTES + C::T_BYTES;
         const uint32_t slot = tmem + quarter + C::SF_COL + (uint32_t)sl * C::SF_SLOT;
@@ -653,10 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
       const Tile t = decode(s, g, tile, NT);
       const float f = NV && g.w_factor ? af * g.w_factor[g.w_factor_per_group ? t.g : 0] : af;
-      int w_ok = 1;
-      if (lane == 0) w_ok = mbar_wait(&s.tfull[acc], acc_phase, abort_flag) ? 1 : 0;
-      w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
-      if (!w_ok) break;
+      if (!warp_wait(&s.tfull[acc], acc_phase, abort_flag)) break;
       tc_fence_after();
       const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 2 * NT);
       const int ch = t.n0 + 32 * q + (lane & ~7);
@@ -950,11 +945,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int kb = 0; kb < g.kstages; ++kb) {
         turn ^= 1;
         if ((turn ^ 1) != set) continue;
-        // one lane waits, the warp follows it
-        int w_ok = 1;
-        if (lane == 0) w_ok = mbar_wait(&s.sland[stage], phase, abort_flag) ? 1 : 0;
-        w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
-        if (!w_ok) { ok = false; break; }
+        ok = warp_wait(&s.sland[stage], phase, abort_flag);
+        if (!ok) break;
         // pieces past the row's end hold an earlier stage's scales: written, never used
         const uint8_t* sf = s.sring[stage] + lane * 16;
         uint4 w[CPS], r[CPS];
@@ -975,13 +967,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           r[p] = off ? make_uint4(a.z, a.w, b.x, b.y) : a;
           r2[p] = off ? make_uint2(b.z, b.w) : make_uint2(b.x, b.y);
         }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&s.sempty[stage]);
-          w_ok = mbar_wait(&s.empty[before], before_phase, abort_flag) ? 1 : 0;
-        }
-        w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
-        if (!w_ok) { ok = false; break; }
+        ok = warp_wait(&s.empty[before], before_phase, abort_flag);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t slot = tmem + quarter + C::SF_COL + (uint32_t)sl * C::SF_SLOT;
 #pragma unroll
@@ -993,8 +980,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        // like the accumulators, TMEM columns are handed over by the tcgen05 fences
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&s.full[ostage]), 0));
+        // Like the accumulators, TMEM columns are handed over by the tcgen05 fences. The place in the
+        // ring is free only now that the stores have taken the scales: an arrival does not wait for
+        // loads that are under way, and those here take long, with the MMAs reading shared memory at
+        // its rate. (Freed after the loads, places were filled again in the middle of them: 88 of 1600
+        // products of 32768 rows, or all, by the wait before it, had channels with a later stage's scales.)
+        if (lane == 0) {
+          mbar_arrive_cluster(mapa_shared(smem_u32(&s.full[ostage]), 0));
+          mbar_arrive(&s.sempty[stage]);
+        }
         ostage += 2;
         if (ostage >= STAGES) ostage -= STAGES;
         sl += 2;
@@ -1026,9 +1020,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (int tile = cluster; tile < total; tile += nclusters) {
       const Tile t = decode(s, g, tile, NT);
       const float f = NV && g.w_factor ? af * g.w_factor[g.w_factor_per_group ? t.g : 0] : af;
-      int w_ok = 1;
-      if (lane == 0) w_ok = mbar_wait(&s.tfull[acc], acc_phase, abort_flag) ? 1 : 0;
-      w_ok = __shfl_sync(0xffffffffu, w_ok, 0);
+      int w_ok = warp_wait(&s.tfull[acc], acc_phase, abort_flag) ? 1 : 0;
       // all four warps of a range leave together: they meet at its barrier
       if (MODE == kSwiglu) {
         if (lane == 0) s.turn_ok[warp - 2] = w_ok;

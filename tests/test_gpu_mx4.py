@@ -322,3 +322,36 @@ def test_ffn_store_and_fused(cuda_device, fmt, counts, H, I):
     n = int(torch.bincount(tok.long()).max())
     # at most n additions, each within half a unit of a partial sum <= mag, and two products
     assert ((acc.double() - want).abs() <= mag * (n + 3) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("rows,groups,N,K", [(16384, 8, 4096, 6144), (640, 32, 4096, 6144)])
+def test_equal_products_agree_bit_for_bit(cuda_device, fmt, rows, groups, N, K):
+    """The same product 200 times, many stages per tile and many tiles per CTA, the rings of both
+    kernels full all the time: no launch may differ from the first in a bit."""
+    g = torch.Generator(device="cuda").manual_seed(31)
+    nb = K // ref.BLOCK[fmt]
+    codes = torch.full((groups, N, K // 2), 0x22, dtype=torch.uint8, device="cuda")      # all 1.0
+    if fmt == "mxfp4":
+        byte = torch.randint(123, 131, (groups, N, nb), dtype=torch.uint8, device="cuda", generator=g)
+        scale, factor = torch.exp2(byte.double() - 127), None
+    else:
+        byte = torch.randint(0x30, 0x48, (groups, N, nb), dtype=torch.uint8, device="cuda", generator=g)
+        scale, factor = byte.view(torch.float8_e4m3fn).double(), torch.ones(groups, device="cuda")
+    w = mx4.from_checkpoint(fmt, codes, byte, factor)
+    off = torch.arange(0, rows + 1, rows // groups, dtype=torch.int32, device="cuda")
+    one = torch.ones(1, device="cuda") if fmt == "nvfp4" else None
+    a = mx4.allocate(fmt, rows, K, groups, off, tensor_scale=one)
+    mx4.quantize(torch.full((rows, K), 6.0, dtype=torch.bfloat16, device="cuda"), a)     # exact: 6, or 1.5 x 4
+    want = (scale.sum(-1) * ref.BLOCK[fmt] * 6.0).repeat_interleave(rows // groups, 0)
+    ws = mx4.gemm_workspace()
+    first, *outs = [torch.empty(rows, N, dtype=torch.bfloat16, device="cuda") for _ in range(5)]
+    mx4.grouped_gemm(a, w, first, ws)
+    # half a step of bf16, and fp32 sums of terms of one sign: 24 stages of 4 products, each off by 2^-22 at most
+    assert bool(((first.double() - want).abs() <= want * (2.0 ** -8 + 96 * 2.0 ** -22)).all())
+    differ = 0
+    for _ in range(50):
+        for out in outs:
+            mx4.grouped_gemm(a, w, out, ws)
+        differ += sum(int(not torch.equal(out, first)) for out in outs)
+    assert differ == 0 and abi.read_device_status(ws) == 0
