@@ -20,24 +20,28 @@
 //    at about the rate that memory has (107 bytes a cycle at N = 192 besides what TMA writes); in
 //    a pair each CTA reads half of the rows. Two accumulators let the epilogue of a tile overlap
 //    the MMAs of the next.
-// Warps:
+// Warps, one CTA:
 //   0           TMA producer: per stage of K = 256 elements (128 bytes, 128-byte swizzle) the
-//               weight boxes, the tile's rows in a few boxes, and (in the pair kernel a warp of
-//               its own, 18) the block scales as plain bulk copies of the 512-byte pieces
-//   1           TMEM owner and MMA issuer (the pair's leader): 4 tcgen05.mma of K = 64 per stage
-//               and weight block
+//               weight boxes, the tile's rows in a few boxes, and the block scales as plain bulk
+//               copies of the 512-byte pieces
+//   1           TMEM owner and MMA issuer: 4 tcgen05.mma of K = 64 per stage and weight block
 //   2-9         epilogue: tcgen05.ld, math, global stores
-//   10-13       scales (pair: 10-17, four warps for every other stage): each warp copies the stage's pieces from shared memory to its lane quarter
+//   10-13       scales: each warp copies the stage's pieces from shared memory to its lane quarter
 //               of TMEM with tcgen05.st (the MMA reads them in all four quarters)
-// The scales of the stages take turns over the TMEM columns that are left, 3 to 5 slots: with fewer
-// slots than stages the scale warps wait, before they overwrite a slot, until the MMAs that read it
-// have completed. (Two slots held the pair kernel up: from one MMA's end to the next scales in TMEM
-// takes about as long as a stage's MMAs; 594 us instead of 390 at 32768 rows.) tcgen05.cp would copy them without
-// these warps, but each copy of 512 bytes holds up the tensor pipe for some 90 cycles (8 to 16
-// copies per stage of 768): 64 experts' gate/up at a decode batch took 214 us with it.
-// A lane of the epilogue reads one channel of 8 rows; the warp turns them around in shared memory,
-// so that a lane has 8 channels of one row, rounds h with one block scale and stores 16 or 32 bytes
-// at once (one channel per lane took 190 us of 750 at 32768 rows, in 2-byte stores).
+// and the pair, in each CTA: 0 the operands' TMA producer, 1 the MMA issuer (the leader's), then 8 or 12
+// epilogue warps, 8 for the scales (four for every other stage) and the scales' TMA producer.
+// tcgen05.cp would copy the scales without these warps, but each copy of 512 bytes holds up the tensor
+// pipe for some 90 cycles (8 to 16 copies per stage of 768): 64 experts' gate/up at a decode batch
+// took 214 us with it.
+// The scales of the stages take turns over the TMEM columns that are left, in the pair 3 slots (NVFP4)
+// or 6: with fewer slots than stages the scale warps wait, before they overwrite a slot, until the MMAs
+// that read it have completed. (Two slots held the pair kernel up: from one MMA's end to the next
+// scales in TMEM takes about as long as a stage's MMAs; 594 us instead of 390 at 32768 rows.)
+// A lane of the epilogue reads one channel of 8 rows; the warp turns them around, so that a lane has 8
+// channels of one row, rounds h with one block scale and stores 16 or 32 bytes at once (one channel
+// per lane took 190 us of 750 at 32768 rows, in 2-byte stores). In the pair kernel, whose MMAs keep
+// shared memory busy, plain products do it by shuffles (352 us instead of 359, and 143 instead of 150
+// for the FFN's down product of 16384 rows); elsewhere it goes through shared memory.
 //
 // Tiles: a group of `count` rows has ceil(count / NT) tiles along its rows; the table is built in
 // shared memory from `offsets` by every CTA, so the host never reads the counts. Columns past
@@ -58,13 +62,9 @@
 namespace moe {
 namespace {
 
-// two per TMEM lane quarter; a third one gains nothing, and its issue slots are missed by the
-// producers and the issuer (387 us instead of 361 at 32768 rows)
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 8;                        // two per TMEM lane quarter
 constexpr int kScaleWarps = 4;
 constexpr int kThreads = 64 + (kEpiWarps + kScaleWarps) * 32;
-constexpr int kScaleProducer = 2 + kEpiWarps + 2 * kScaleWarps;    // pair kernel: 8 scale warps, and one more
-constexpr int kPairThreads = (kScaleProducer + 1) * 32;
 constexpr uint32_t kTmemCols = 512;
 // a warp's staging rows: 8 rows of 32 channels, 4 floats apart from a multiple of 32, so that
 // neither the writes (a row at a time) nor the reads (16 bytes of 8 rows) meet in a bank
@@ -77,6 +77,12 @@ constexpr int W_BYTES = 128 * 128;                  // a weight block's stage: 1
 
 // kStore: y in bf16; kFp32: y in fp32, stored or added to the tokens' sums; kSwiglu: h in 4 bits
 enum Mode : int { kStore = 0, kFp32 = 1, kSwiglu = 2 };
+
+// Pair kernel: plain products have a third epilogue warp per quarter (17081 rows of the 768-wide layer
+// in 20.2 us instead of 21.5). The rounding of h gains nothing by one, and it takes issue slots from the
+// other roles (229 to 236 us instead of 221 for 16384 rows' gate and up).
+constexpr int pair_epi_warps(int mode) { return mode == kSwiglu ? kEpiWarps : 12; }
+constexpr int pair_threads(int mode) { return (2 + pair_epi_warps(mode) + 2 * kScaleWarps + 1) * 32; }
 
 struct Args {
   Mx4Rows a;              // the rows' groups
@@ -295,6 +301,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
 
+// tmem_ld_wait, with what was loaded: no use of it moves above the wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[N]) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i])::"memory");
+}
+
 // Whether the phase of the given parity is over, without waiting for it.
 __device__ __forceinline__ uint32_t mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -337,6 +351,43 @@ __device__ __forceinline__ void turn_around(float (&v)[8], float (*stg)[kStageLd
   __syncwarp();                // the rows may be written again
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// The same in registers: in step b = 1, 2, 4, lanes l and l ^ b exchange the halves that the other keeps.
+__device__ __forceinline__ void turn_in_registers(float (&v)[8], int lane) {
+#pragma unroll
+  for (int b = 1; b < 8; b <<= 1) {
+    const bool up = lane & b;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j & b) continue;
+      const float got = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j | b], b);
+      if (up) v[j] = got;
+      else v[j | b] = got;
+    }
+  }
+}
+// And rounded to bf16 on the way, two rows (then two channels) in a register.
+__device__ __forceinline__ uint4 turn_to_bf16(const float (&v)[8], float f, int lane) {
+  uint32_t q[4];
+  const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;      // (got, own) high halves, or (own, got) low ones
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t own = pack_bf16x2(v[2 * k] * f, v[2 * k + 1] * f);
+    q[k] = __byte_perm(own, __shfl_xor_sync(0xffffffffu, own, 1), sel);
+  }
+#pragma unroll
+  for (int b = 1; b < 4; b <<= 1) {
+    const bool up = lane & (2 * b);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k & b) continue;
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? q[k] : q[k | b], 2 * b);
+      if (up) q[k] = got;
+      else q[k | b] = got;
+    }
+  }
+  return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
 // The scale byte of a block of h with the largest magnitude top (as bits) and what its values are
@@ -418,6 +469,20 @@ __device__ __forceinline__ void epi_store(const Args& a, const Tile& t, int c, i
       if (add) atomicAdd(dst + i, s * v[i]);
       else dst[i] = v[i];
     }
+  }
+}
+
+// y in bf16, rounded before it was turned around.
+__device__ __forceinline__ void epi_store_bf16(const Args& a, const Tile& t, int c, int ch, int lane, const uint4& q) {
+  if (c + (lane & 7) >= t.n || ch >= a.n_out) return;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (size_t)(t.row0 + c + (lane & 7)) * a.n_out + ch;
+  if ((a.n_out & 7) == 0) {
+    *reinterpret_cast<uint4*>(dst) = q;
+  } else {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (ch + i < a.n_out) reinterpret_cast<uint16_t*>(dst)[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
   }
 }
 
@@ -746,13 +811,13 @@ __device__ __forceinline__ void epi_round_h_pair(const Args& a, const Tile& t, i
 __device__ __forceinline__ void range_bar(int part) { asm volatile("bar.sync %0, 128;" ::"r"(part + 1) : "memory"); }
 
 template <int CPS, int MODE>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(pair_threads(MODE), 1)
     k_mx4_gemm_pair(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA96,
                     const __grid_constant__ CUtensorMap tmA16, const __grid_constant__ CUtensorMap tmSW,
                     const __grid_constant__ CUtensorMap tmSA, const Args g) {
   using C = Pair<CPS>;
   constexpr bool NV = CPS == 4;
-  constexpr int STAGES = C::STAGES, NT = C::NT;
+  constexpr int STAGES = C::STAGES, NT = C::NT, EPI = pair_epi_warps(MODE);
   extern __shared__ uint8_t smem_raw[];
   auto& s = *reinterpret_cast<Storage<C>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -772,7 +837,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.tfull[i], 1);
-      mbar_init(&s.tempty[i], 2 * kEpiWarps);
+      mbar_init(&s.tempty[i], 2 * EPI);
     }
     s.abort_flag = 0;
     fence_barrier_init();
@@ -838,7 +903,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (next == 0) phase ^= 1u;
       }
     }
-  } else if (warp == kScaleProducer) {
+  } else if (warp == 2 + EPI + 2 * kScaleWarps) {
     // ---- TMA producer of the scales, counted on this CTA, into a ring that the scale warps free
     // as soon as they have read a stage. Always two scale tiles of rows: what the tile does not have
     // of them is any group's or zeros, and not used ----------------------------------------------
@@ -921,11 +986,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
-  } else if (warp >= 2 + kEpiWarps) {
+  } else if (warp >= 2 + EPI) {
     // ---- scales of both CTAs: shared memory -> this warp's lane quarter of TMEM. A stage takes a
     // warp some 560 cycles, longer than its MMAs: two sets of four warps take turns ---------------
     const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
-    const int set = (warp - 2 - kEpiWarps) / kScaleWarps;
+    const int set = (warp - 2 - EPI) / kScaleWarps;
     int turn = 0;                // of the set whose stage it is
     int stage = set;             // this set's next one, of the scales' ring,
     uint32_t phase = 0;
@@ -1006,11 +1071,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     }
   } else {
-    // ---- epilogue (both CTAs): this CTA's 128 weight rows; the two warps of a quarter take
-    // turns over chunks of 16 columns -----------------------------------------------------------
+    // ---- epilogue (both CTAs): this CTA's 128 weight rows; the warps of a quarter take turns
+    // over chunks of 16 columns -----------------------------------------------------------
     const int q = warp & 3;
     const int part = (warp - 2) >> 2;
-    float (*stg)[kStageLd] = reinterpret_cast<float (*)[kStageLd]>(s.turn + (warp - 2) * 8 * kStageLd);
     float (*S)[kGroupLd] = reinterpret_cast<float (*)[kGroupLd]>(s.turn + part * 8 * kGroupLd);
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -1032,10 +1096,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       tc_fence_after();
       const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * NT);
 #pragma unroll 1
-      for (int c = 16 * part; c < t.n; c += 16 * (kEpiWarps / 4)) {
+      for (int c = 16 * part; c < t.n; c += 16 * (EPI / 4)) {
         uint32_t v[16];
         tmem_ld_32x32b_x16(base + c, v);
-        tmem_ld_wait();
+        tmem_ld_wait_for(v);
         if constexpr (MODE == kSwiglu) {
 #pragma unroll
           for (int e = 0; e < 16; e += 8) {
@@ -1051,8 +1115,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             float x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(v[e + j]);
-            turn_around(x, stg, lane);
-            epi_store<MODE>(g, t, c + e, t.n0 + 128 * (int)rank + 32 * q + (lane & ~7), lane, f, x);
+            const int ch = t.n0 + 128 * (int)rank + 32 * q + (lane & ~7);
+            if constexpr (MODE == kStore) {
+              epi_store_bf16(g, t, c + e, ch, lane, turn_to_bf16(x, f, lane));
+            } else {
+              turn_in_registers(x, lane);
+              epi_store<MODE>(g, t, c + e, ch, lane, f, x);
+            }
             __syncwarp();
           }
         }
@@ -1144,7 +1213,7 @@ int launch_pair(const moe_mx4_t& a, const moe_mx4_t& w, const Args& g, const Dev
       attr[0].val.clusterDim.y = 1;
       attr[0].val.clusterDim.z = 1;
       cfg.gridDim = dim3(dev.sm_count & ~1);
-      cfg.blockDim = dim3(kPairThreads);
+      cfg.blockDim = dim3(pair_threads(MODE));
       cfg.dynamicSmemBytes = smem;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
@@ -1157,7 +1226,7 @@ int launch_pair(const moe_mx4_t& a, const moe_mx4_t& w, const Args& g, const Dev
     }
     n = clusters_of[dev.device];
   }
-  const cudaError_t e = launch_kernel(kern, 2 * n, kPairThreads, smem, st, 2, mw, a96, a16, sw, sa, g);
+  const cudaError_t e = launch_kernel(kern, 2 * n, pair_threads(MODE), smem, st, 2, mw, a96, a16, sw, sa, g);
   count_launch();
   return cuda_rc(e);
 }
