@@ -1,15 +1,18 @@
 // mx4_quant.cu - rows to microscaled 4 bits and back, and a checkpoint's scales into the
 // tensor cores' layout (moe_mx4_quantize, moe_mx4_dequantize, moe_mx4_pack_scales).
 //
-// Every kernel here moves bytes: per element 2 (bf16) or 4 (fp32) on one side and 0.5 plus the
-// block's share of a scale byte on the other, against a dozen instructions. One lane holds 8
-// elements (16 bytes of bf16, 4 bytes of codes), so a warp moves 512 contiguous bytes in and
-// 128 out; a block's largest magnitude is a butterfly over its 4 (MXFP4) or 2 (NVFP4) lanes,
-// and the four scale bytes of a piece's row go out as one word. A warp takes up to 6 steps of
-// 256 elements of a row, all their loads in flight at once, and looks for the row's group once for
-// them: 32768 rows of 6144 to MXFP4 took 208, 147, 118, 107 and 121 us with 1, 2, 4, 6 and 8 steps.
-// The number of steps is the smallest that covers a row in as few warps (6 steps for rows of 768
-// leave half of the lanes' work empty: 36 us for 17081 rows instead of 20).
+// Every kernel here moves bytes: per element 2 (bf16) or 4 (fp32) on one side and 0.5 plus the block's
+// share of a scale byte on the other, against a few instructions, and both sides have to be kept low.
+//  * quantise: a lane holds 16 elements (32 bytes of bf16 in one load, 8 bytes of codes), which are an
+//    NVFP4 block, or half of an MXFP4 one whose largest magnitude takes one shuffle; the four scale
+//    bytes of a piece's row go out as one word. With 8 elements per lane twice as many lanes worked out
+//    each scale: 8192 rows of 6144 to NVFP4 took 35.6 us instead of 26.1 (4.9 TB/s), 32768 to MXFP4 89
+//    instead of 76 (6.6 TB/s, the card's copy rate). A warp takes up to 3 steps of 512 elements of a row
+//    (4 steps: 74.8 and 26.3 us, and 2.24 instead of 2.05 for 128 rows), all their loads in flight at
+//    once, and looks for the row's group once for them.
+//  * dequantise: 8 elements per lane, up to 6 steps of 256 elements per warp (23 us for 8192 rows of
+//    6144 from NVFP4; 33.5 with the values made by integer operations instead of conversions).
+// The number of steps is the smallest that covers a row in as few warps.
 #include "checks.cuh"
 #include "kernels.cuh"
 #include "launch.cuh"
@@ -18,27 +21,10 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxSteps = 6;                  // 256-element steps of a warp
+constexpr int kQuantSteps = 3;                // of a warp, of 512 elements
+constexpr int kDequantSteps = 6;              // of 256
 constexpr int kQuantThreads = 128;
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-template <>
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
@@ -47,6 +33,51 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
+
+// 16 elements as they are in memory: 32 bytes in one load where they are aligned to that, else in two.
+template <typename T>
+struct Sixteen {
+  uint4 q[sizeof(T)];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) q[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void load(const T* p, bool wide) {
+    const uint4* s = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); i += 2) {
+      if (wide) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w), "=r"(q[i + 1].x), "=r"(q[i + 1].y),
+                       "=r"(q[i + 1].z), "=r"(q[i + 1].w)
+                     : "l"(s + i));
+      } else {
+        q[i] = s[i];
+        q[i + 1] = s[i + 1];
+      }
+    }
+  }
+  // elements 8 h to 8 h + 7
+  __device__ __forceinline__ void half(int h, float (&v)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w[4] = {q[h].x, q[h].y, q[h].z, q[h].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4& a = q[2 * h + i];
+        v[4 * i] = __uint_as_float(a.x);
+        v[4 * i + 1] = __uint_as_float(a.y);
+        v[4 * i + 2] = __uint_as_float(a.z);
+        v[4 * i + 3] = __uint_as_float(a.w);
+      }
+    }
+  }
+};
 
 struct QuantArgs {
   Mx4Rows m;
@@ -59,9 +90,10 @@ struct QuantArgs {
   uint8_t* codes;
   uint8_t* scales;
   int* status;
+  bool wide;                // rows of x are 32-byte aligned
 };
 
-// One warp: S steps of 256 elements of one row of x, to one row of m or to the rows of its picks.
+// One warp: S steps of 512 elements of one row of x, to one row of m or to the rows of its picks.
 template <typename T, bool NV, int S>
 __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const QuantArgs q) {
   pdl_launch_dependents();
@@ -69,7 +101,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const QuantArgs 
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5);
   if (t >= q.tokens) return;
-  const int k0 = blockIdx.y * (S * 256);
+  const int k0 = blockIdx.y * (S * 512);
   const int chunks = q.m.K / (4 * mx4_block(NV));
   // the destinations: lane p holds pick p's row
   int dst = -1;
@@ -81,16 +113,12 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const QuantArgs 
   unsigned left = __ballot_sync(0xffffffffu, dst >= 0);
   if (!left) return;
   const T* src = static_cast<const T*>(q.x) + (int64_t)t * q.ld;
-  float v[S][8];
+  Sixteen<T> v[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    const int k = k0 + s * 256 + lane * 8;
-    if (k < q.m.K) {
-      load8(src + k, v[s]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[s][i] = 0.f;
-    }
+    const int k = k0 + s * 512 + lane * 16;
+    if (k < q.m.K) v[s].load(src + k, q.wide);
+    else v[s].clear();
   }
   // its group, looked for while the loads are under way: of the row, or of lane p's pick
   int g, o_g = 0, row = t;
@@ -105,19 +133,23 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const QuantArgs 
   const int my_g = g, my_o = o_g;
   const Mx4Factor f = mx4_factor(NV && q.factor ? q.factor[q.factor_per_group ? g : 0] : 1.0f);
 
-  uint32_t code[S], scale[S];
+  constexpr int kLanes = mx4_block(NV) / 16;      // of a block
+  uint2 code[S];
+  uint32_t scale[S];
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max_abs(top, v[s][i]);
-#pragma unroll
-    for (int o = 1; o < mx4_block(NV) / 8; o <<= 1) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float a[8], b[8];
+    v[s].half(0, a);
+    v[s].half(1, b);
+    float top = max_abs(max_abs(a[0], a[1], a[2]), a[3], a[4]);
+    top = max_abs(max_abs(top, a[5], a[6]), a[7], b[0]);
+    top = max_abs(max_abs(top, b[1], b[2]), b[3], b[4]);
+    top = max_abs(max_abs(top, b[5], b[6]), b[7]);
+    if (kLanes == 2) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
     float by;
     const uint32_t byte = mx4_scale<NV>(top, f, by);
-    code[s] = mx4_codes<NV>(v[s], by);
-    // the four scales of one piece's row, gathered from its 16 (8) lanes into a word
-    constexpr int kLanes = mx4_block(NV) / 8;
+    code[s] = make_uint2(mx4_codes<NV>(a, by), mx4_codes<NV>(b, by));
+    // the four scales of one piece's row, gathered from its 8 (4) lanes into a word
     uint32_t w = byte << (8 * ((lane / kLanes) & 3));
     w |= __shfl_xor_sync(0xffffffffu, w, kLanes);
     w |= __shfl_xor_sync(0xffffffffu, w, 2 * kLanes);
@@ -132,13 +164,12 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const QuantArgs 
       o_g = __shfl_sync(0xffffffffu, my_o, p);
     }
     uint8_t* codes = q.codes + (int64_t)row * (q.m.K / 2);
-    constexpr int kPiece = mx4_block(NV) / 2;     // lanes of a piece's row: 4 blocks of 8-element lanes
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int k = k0 + s * 256 + lane * 8;
+      const int k = k0 + s * 512 + lane * 16;
       if (k < q.m.K) {
-        *reinterpret_cast<uint32_t*>(codes + k / 2) = code[s];
-        if ((lane & (kPiece - 1)) == 0)
+        *reinterpret_cast<uint2*>(codes + k / 2) = code[s];
+        if ((lane & (4 * kLanes - 1)) == 0)
           *reinterpret_cast<uint32_t*>(q.scales + mx4_scale_at(o_g, g, row - o_g, k / mx4_block(NV), chunks)) =
               scale[s];
       }
@@ -185,13 +216,9 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_dequantize(const DequantA
     const int k = k0 + s * 256 + lane * 8;
     const float sc = NV ? __fmul_rn(e4m3_value(byte[s]), f) : e8m0_value(byte[s]);
     float v[8];
+    e2m1x8_values(code[s], v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // magnitude code m: 0, 0.5, then 1 + half a low bit with exponent m / 2 - 1
-      const uint32_t c = code[s] >> (4 * i), m = c & 7u;
-      const uint32_t bits = m < 2u ? (m ? 0x3F000000u : 0u) : ((126u + (m >> 1)) << 23) | ((m & 1u) << 22);
-      v[i] = __fmul_rn(__uint_as_float(bits | ((c & 8u) << 28)), sc);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], sc);
     if (k < q.m.K) store8(static_cast<T*>(q.out) + (int64_t)row * q.ld + k, v);
   }
 }
@@ -212,10 +239,11 @@ __global__ void __launch_bounds__(256) k_mx4_pack_scales(const Mx4Rows m, int ch
   }
 }
 
-// The grid of one warp per S steps of each row, and S; MOE_ERR_UNSUPPORTED beyond the grid's limit.
-int step_grid(int rows, int K, dim3* grid, int* S) {
-  const int steps = (K + 255) / 256;
-  const int warps = (steps + kMaxSteps - 1) / kMaxSteps;         // along a row
+// The grid of one warp per S steps (at most most, of `step` elements) of each row, and S;
+// MOE_ERR_UNSUPPORTED beyond the grid's limit.
+int step_grid(int rows, int K, int step, int most, dim3* grid, int* S) {
+  const int steps = (K + step - 1) / step;
+  const int warps = (steps + most - 1) / most;                   // along a row
   *S = (steps + warps - 1) / warps;
   if (*S == 5) *S = 6;                                           // not built
   if (warps > 65535) return MOE_ERR_UNSUPPORTED;
@@ -223,11 +251,14 @@ int step_grid(int rows, int K, dim3* grid, int* S) {
   return MOE_OK;
 }
 
-#define MX4_STEPS(KERN, T, NV) \
-  (S == 1 ? KERN<T, NV, 1> : S == 2 ? KERN<T, NV, 2> : S == 3 ? KERN<T, NV, 3> : S == 4 ? KERN<T, NV, 4> : KERN<T, NV, 6>)
-#define MX4_KERNEL(KERN)                                                                              \
-  (dtype == MOE_BF16 ? (is_nv(*m) ? MX4_STEPS(KERN, __nv_bfloat16, true) : MX4_STEPS(KERN, __nv_bfloat16, false)) \
-                     : (is_nv(*m) ? MX4_STEPS(KERN, float, true) : MX4_STEPS(KERN, float, false)))
+#define MX4_QUANT(T, NV) \
+  (S == 1 ? k_mx4_quantize<T, NV, 1> : S == 2 ? k_mx4_quantize<T, NV, 2> : k_mx4_quantize<T, NV, 3>)
+#define MX4_DEQUANT(T, NV)                                                                                   \
+  (S == 1 ? k_mx4_dequantize<T, NV, 1> : S == 2 ? k_mx4_dequantize<T, NV, 2> : S == 3 ? k_mx4_dequantize<T, NV, 3> \
+   : S == 4 ? k_mx4_dequantize<T, NV, 4> : k_mx4_dequantize<T, NV, 6>)
+#define MX4_KERNEL(WHICH)                                                              \
+  (dtype == MOE_BF16 ? (is_nv(*m) ? WHICH(__nv_bfloat16, true) : WHICH(__nv_bfloat16, false)) \
+                     : (is_nv(*m) ? WHICH(float, true) : WHICH(float, false)))
 
 int check_ld(const moe_mx4_t* m, int32_t dtype, int64_t ld) {
   if (dtype != MOE_BF16 && dtype != MOE_FP32) return MOE_ERR_INVALID_ARG;
@@ -296,7 +327,7 @@ int moe_mx4_quantize(const moe_mx4_t* m, const void* x, int32_t dtype, int64_t l
   QuantArgs q{};
   dim3 grid;
   int S;
-  MOE_TRY(step_grid(tokens, m->K, &grid, &S));
+  MOE_TRY(step_grid(tokens, m->K, 512, kQuantSteps, &grid, &S));
   DeviceInfo dev;
   MOE_TRY(current_device_info(&dev));
   q.m = mx4_rows(*m);
@@ -310,7 +341,8 @@ int moe_mx4_quantize(const moe_mx4_t* m, const void* x, int32_t dtype, int64_t l
   q.codes = static_cast<uint8_t*>(m->codes);
   q.scales = static_cast<uint8_t*>(m->scales);
   q.status = status;
-  auto kern = MX4_KERNEL(k_mx4_quantize);
+  q.wide = (reinterpret_cast<uintptr_t>(x) | (uintptr_t)(ld * (dtype == MOE_BF16 ? 2 : 4))) % 32 == 0;
+  auto kern = MX4_KERNEL(MX4_QUANT);
   const cudaError_t e = launch_kernel(kern, grid, kQuantThreads, 0, as_stream(stream), 1, q);
   count_launch();
   return cuda_rc(e);
@@ -323,7 +355,7 @@ int moe_mx4_dequantize(const moe_mx4_t* m, void* out, int32_t dtype, int64_t ld,
   MOE_TRY(check_ptrs({out, m->codes, m->scales}));
   dim3 grid;
   int S;
-  MOE_TRY(step_grid(m->rows, m->K, &grid, &S));
+  MOE_TRY(step_grid(m->rows, m->K, 256, kDequantSteps, &grid, &S));
   DeviceInfo dev;
   MOE_TRY(current_device_info(&dev));
   DequantArgs q{};
@@ -334,7 +366,7 @@ int moe_mx4_dequantize(const moe_mx4_t* m, void* out, int32_t dtype, int64_t ld,
   q.scales = static_cast<const uint8_t*>(m->scales);
   q.out = out;
   q.ld = ld;
-  auto kern = MX4_KERNEL(k_mx4_dequantize);
+  auto kern = MX4_KERNEL(MX4_DEQUANT);
   const cudaError_t e = launch_kernel(kern, grid, kQuantThreads, 0, as_stream(stream), 1, q);
   count_launch();
   return cuda_rc(e);

@@ -355,3 +355,28 @@ def test_equal_products_agree_bit_for_bit(cuda_device, fmt, rows, groups, N, K):
             mx4.grouped_gemm(a, w, out, ws)
         differ += sum(int(not torch.equal(out, first)) for out in outs)
     assert differ == 0 and abi.read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K,shift,pad", [(128, 0, 8), (640, 8, 0), (1024, 8, 8), (1664, 0, 8), (1664, 16, 16), (2688, 8, 24)])
+def test_rows_aligned_to_16_bytes_only(cuda_device, fmt, dtype, K, shift, pad):
+    """Starts and strides of odd multiples of 16 bytes (and of 32), blocks of zeros and rows that end
+    inside a warp's step: the bits of the formula."""
+    g = torch.Generator(device="cuda").manual_seed(K + shift)
+    per = 16 // dtype.itemsize                       # elements of 16 bytes
+    shift, pad = shift // 8 * per, pad // 8 * per
+    buf = torch.randn(37, shift + K + pad, device="cuda", generator=g).to(dtype)
+    x = buf[:, shift:shift + K]
+    x[::3, 32:64] = 0.0
+    x[5] = 0.0
+    t = torch.full((1,), 2.0 ** -6, device="cuda") if fmt == "nvfp4" else None
+    m = mx4.allocate(fmt, 37, K, tensor_scale=t)
+    mx4.quantize(x, m)
+    codes, byte, value = ref.quantize(x, fmt, float(t) if t is not None else 1.0)
+    assert torch.equal(m.codes, ref.pack(codes).to(torch.uint8))
+    at = ref.scale_index([0, 37], K, fmt, "cuda")
+    assert torch.equal(m.scales.flatten()[at].int(), byte.int())
+    out = torch.empty(37, K, dtype=torch.float32, device="cuda")
+    mx4.dequantize(m, out)
+    assert torch.equal(out.double(), value)
