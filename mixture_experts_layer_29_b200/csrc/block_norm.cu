@@ -11,7 +11,8 @@
 //   d_gate = s sum g n1,  d_w_post = sum_t dn1 bhat,  d_w_pre = sum_t d_n2 rhat
 //
 // Bound by memory: 4 rows of H elements in and out per token forward, 6 backward, against some
-// 10 and 22 flops per element. One CTA holds a token's row in registers (16-byte vectors), so
+// 10 and 22 flops per element (the backward's done two at a time: 119 us instead of 123 for 8192 x 6144
+// bf16, 151 instead of 186 for 4096 x 8192). One CTA holds a token's row in registers (16-byte vectors), so
 // each array is read once; the two norms are two block reductions in a row, the second on what
 // the first produced. Forward: one CTA per token. Backward: persistent CTAs, so that the sums
 // over tokens (d_w_post, d_w_pre, d_gate per channel) stay in registers; each CTA writes its
@@ -195,6 +196,21 @@ __device__ __forceinline__ TokenScalars load_scalars(const BwdArgs& a, size_t t)
                       a.gate == MOE_GATE_TOKEN ? a.g[t] : 1.f};
 }
 
+// Elements j and j + 1 as a register pair, back, and their sum.
+template <int N>
+__device__ __forceinline__ uint64_t pair(const float (&v)[N], int j) {
+  return pack_f32x2(v[j], v[j + 1]);
+}
+template <int N>
+__device__ __forceinline__ void put(uint64_t p, float (&v)[N], int j) {
+  unpack_f32x2(p, v[j], v[j + 1]);
+}
+__device__ __forceinline__ float both(uint64_t p) {
+  float a, b;
+  unpack_f32x2(p, a, b);
+  return a + b;
+}
+
 // One token's gradients, for the VPT vectors of a thread: its rows (d_normed and res_out unpacked into
 // g and rhat, d_res_out and block as loaded) and its sums over tokens. wg = w_post * gate of the column;
 // the sum p of gate_t g bhat serves both d_w_post (scale * gate_c * p) and d_gate_c (scale * w_post * p).
@@ -208,30 +224,37 @@ __device__ __forceinline__ void token_gradients(const BwdArgs& a, size_t t, int 
   const size_t o = t * a.H;
   float sum = 0.f;
   if (a.w_pre) {
+    const uint64_t rr = pack_f32x2(k.rr, k.rr);
+    uint64_t sums = 0;                                      // of the even and of the odd elements
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       float w[N];
       w_pre(i, w);
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        rhat[i][j] *= k.rr;
-        s_pre[i][j] = fmaf(g[i][j], rhat[i][j], s_pre[i][j]);
-        g[i][j] *= w[j];                                    // c
-        sum = fmaf(g[i][j], rhat[i][j], sum);
+      for (int j = 0; j < N; j += 2) {
+        const uint64_t rh = mul_f32x2(pair(rhat[i], j), rr);
+        put(fma_f32x2(pair(g[i], j), rh, pair(s_pre[i], j)), s_pre[i], j);
+        const uint64_t c = mul_f32x2(pair(g[i], j), pair(w, j));
+        sums = fma_f32x2(c, rh, sums);
+        put(rh, rhat[i], j);
+        put(c, g[i], j);
       }
     }
+    sum = both(sums);
     sum = block_sum(sum, part[0]) * inv_h;
   } else {
     __syncthreads();
   }
   // g: the gradient of the residual stream
+  const uint64_t rr = pack_f32x2(k.rr, k.rr), minus = pack_f32x2(-sum, -sum);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     float d[N];
     Row<T>::unpack(qd[i], d);
 #pragma unroll
-    for (int j = 0; j < N; ++j) g[i][j] = fmaf(k.rr, g[i][j] - rhat[i][j] * sum, d[j]);
+    for (int j = 0; j < N; j += 2)
+      put(fma_f32x2(rr, fma_f32x2(pair(rhat[i], j), minus, pair(g[i], j)), pair(d, j)), g[i], j);
     if (v < nvec) reinterpret_cast<uint4*>(static_cast<T*>(a.d_residual) + o)[v] = Row<T>::pack(g[i]);
   }
   if (!a.block) {
@@ -239,21 +262,23 @@ __device__ __forceinline__ void token_gradients(const BwdArgs& a, size_t t, int 
     return;
   }
   // bhat in rhat's registers
-  float dot = 0.f;                                          // <g wg, bhat>
+  uint64_t dots = 0;                                        // <g wg, bhat>
+  const uint64_t rb = pack_f32x2(k.rb, k.rb), gt = pack_f32x2(k.gt, k.gt);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    float w[N];
+    float w[N], b[N];
     wg(i, w);
-    Row<T>::unpack(qb[i], rhat[i]);
+    Row<T>::unpack(qb[i], b);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      rhat[i][j] *= k.rb;
-      const float h = g[i][j] * rhat[i][j];
-      s_post[i][j] = fmaf(k.gt, h, s_post[i][j]);
-      dot = fmaf(h, w[j], dot);
-      g[i][j] *= w[j];
+    for (int j = 0; j < N; j += 2) {
+      const uint64_t bh = mul_f32x2(pair(b, j), rb), h = mul_f32x2(pair(g[i], j), bh);
+      put(fma_f32x2(gt, h, pair(s_post[i], j)), s_post[i], j);
+      dots = fma_f32x2(h, pair(w, j), dots);
+      put(mul_f32x2(pair(g[i], j), pair(w, j)), g[i], j);
+      put(bh, rhat[i], j);
     }
   }
+  float dot = both(dots);
   float mean = 0.f;
   if (a.w_post || a.gate == MOE_GATE_TOKEN) {
     dot = block_sum(dot, part[1]);
@@ -261,11 +286,13 @@ __device__ __forceinline__ void token_gradients(const BwdArgs& a, size_t t, int 
     if (a.w_post) mean = dot * inv_h;
   }
   const float f = a.scale * k.gt * k.rb;
+  const uint64_t ff = pack_f32x2(f, f), less = pack_f32x2(-mean, -mean);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
 #pragma unroll
-    for (int j = 0; j < N; ++j) g[i][j] = f * (g[i][j] - rhat[i][j] * mean);
+    for (int j = 0; j < N; j += 2)
+      put(mul_f32x2(ff, fma_f32x2(pair(rhat[i], j), less, pair(g[i], j))), g[i], j);
     if (v < nvec) reinterpret_cast<uint4*>(static_cast<T*>(a.d_block) + o)[v] = Row<T>::pack(g[i]);
   }
   // part[0] may be written again: every thread has read it before the second sum's barrier
@@ -337,11 +364,14 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd(const BwdArgs a) {
 // Rows through a ring in shared memory, filled by bulk copies: a CTA of a wide row has an SM to itself
 // (its sums over tokens stay in registers), so the loads of the next tokens go on under the two block
 // reductions of this one. (Loading the next token into registers instead gained nothing: 169 us for
-// 8192 x 6144 bf16.) The ring has `depth` tokens of up to four rows.
+// 8192 x 6144 bf16.) The ring has `depth` tokens of up to four rows. A CTA of at most 512 threads may use
+// 128 registers a thread: with the parameters and both vectors' sums in them 4096 x 8192 bf16 take 86 us
+// instead of 148 with the parameters read for every token, 4096 x 6144 fp32 119 instead of 137.
 constexpr int kMaxDepth = 4;
+constexpr int kRingThreads = 768;      // what the register file holds with their sums
 
-template <typename T, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 768 : 1024) k_block_norm_bwd_ring(const BwdArgs a, int depth) {
+template <typename T, int VPT, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_block_norm_bwd_ring(const BwdArgs a, int depth) {
   constexpr int N = Row<T>::N;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float part[2][32];
@@ -370,12 +400,11 @@ __global__ void __launch_bounds__(VPT == 1 ? 768 : 1024) k_block_norm_bwd_ring(c
     for (int s = 0; s < depth; ++s)
       if (blockIdx.x + (size_t)s * gridDim.x < (size_t)a.T) fill(s, blockIdx.x + (size_t)s * gridDim.x);
 
-  // the columns' parameters stay in registers where a thread has one vector
+  // the columns' parameters stay in registers
   float wp[VPT][N], wg[VPT][N];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = min((int)(threadIdx.x + i * blockDim.x), nvec - 1) * N;
-    if (VPT > 1) continue;
     if (a.w_pre) load_param(a.w_pre, c, wp[i]);
     load_wg(a, c, wg[i]);
   }
@@ -404,24 +433,16 @@ __global__ void __launch_bounds__(VPT == 1 ? 768 : 1024) k_block_norm_bwd_ring(c
     token_gradients<T, VPT>(
         a, t, nvec, g, rhat, qd, qb, k, inv_h, s_post, s_pre, part,
         [&](int i, float (&w)[N]) {
-          if (VPT > 1) {
-            load_param(a.w_pre, min((int)(threadIdx.x + i * blockDim.x), nvec - 1) * N, w);
-          } else {
 #pragma unroll
-            for (int j = 0; j < N; ++j) w[j] = wp[i][j];
-          }
+          for (int j = 0; j < N; ++j) w[j] = wp[i][j];
         },
         [&](int i, float (&w)[N]) {
-          if (VPT > 1) {
-            load_wg(a, min((int)(threadIdx.x + i * blockDim.x), nvec - 1) * N, w);
-          } else {
 #pragma unroll
-            for (int j = 0; j < N; ++j) w[j] = wg[i][j];
-          }
+          for (int j = 0; j < N; ++j) w[j] = wg[i][j];
         });
     // every thread has used its rows before the token's last barrier (loads that are only under way
     // there would not do): the place is free. Filling it at the end of the token keeps the copies'
-    // issue, some 140 cycles each, out of the block's way (115 us instead of 132 for 8192 x 6144 bf16)
+    // issue, some 140 cycles each, out of the block's way (17 us of 132 for 8192 x 6144 bf16)
     const size_t next = t + (size_t)depth * gridDim.x;
     if (threadIdx.x == 0 && next < (size_t)a.T) fill(s, next);
     if (++s == depth) {
@@ -489,9 +510,9 @@ void row_shape(int nvec, int most, int* vpt, int* threads) {
   *threads = ((nvec + *vpt - 1) / *vpt + 31) / 32 * 32;
 }
 
-// The backward's CTAs. With the ring: up to 768 threads of one or two vectors (768 is what the register
-// file holds with their sums), up to 1024 of wider rows; as many CTAs as make up 768 threads per SM.
-// Without (depth 0: less than two tokens' rows fit): 1024 threads, one CTA per SM.
+// The backward's CTAs. With the ring, for rows of up to 2 x 768 vectors of which two tokens' fit: up to 768
+// threads of one or two vectors, as many CTAs as make up 768 threads per SM. Without (depth 0): up to 1024
+// threads, one CTA per SM.
 struct BwdShape {
   int vpt, threads, per_sm, depth;
   size_t smem;
@@ -500,10 +521,11 @@ BwdShape bwd_shape(const moe_norm_t& n) {
   BwdShape b{};
   const size_t esz = n.dtype == MOE_BF16 ? 2 : 4, token = 4 * esz * n.H;
   const int nvec = (int)(n.H * esz / 16);
-  row_shape(nvec, nvec <= 1536 ? 768 : 1024, &b.vpt, &b.threads);
-  b.per_sm = max(1, 768 / b.threads);
+  const bool narrow = nvec <= 2 * kRingThreads;
+  row_shape(nvec, narrow ? kRingThreads : 1024, &b.vpt, &b.threads);
+  b.per_sm = max(1, kRingThreads / b.threads);
   b.depth = (int)min((size_t)kMaxDepth, (size_t)200 * 1024 / b.per_sm / token);
-  if (b.depth < 2) b.depth = 0;
+  if (b.depth < 2 || !narrow) b.depth = 0;
   b.smem = b.depth * token;
   return b;
 }
@@ -591,16 +613,23 @@ int moe_block_norm_backward(const moe_norm_t* n, const void* d_residual_out, con
   const bool bf16 = n->dtype == MOE_BF16;
   const BwdShape b = bwd_shape(*n);
   const int grid = min(n->T, min(dev.sm_count, kMaxSms) * b.per_sm);
-#define NORM_BWD(KERN, T) (b.vpt == 1 ? KERN<T, 1> : b.vpt == 2 ? KERN<T, 2> : b.vpt == 3 ? KERN<T, 3> : KERN<T, 4>)
   if (n->T > 0) {
     cudaError_t e;
     if (b.depth) {
-      auto kern = bf16 ? NORM_BWD(k_block_norm_bwd_ring, __nv_bfloat16) : NORM_BWD(k_block_norm_bwd_ring, float);
+#define NORM_RING(T)                                                      \
+  (b.vpt == 1            ? k_block_norm_bwd_ring<T, 1, kRingThreads>       \
+   : b.threads <= 512    ? k_block_norm_bwd_ring<T, 2, 512>                \
+                         : k_block_norm_bwd_ring<T, 2, kRingThreads>)
+      auto kern = bf16 ? NORM_RING(__nv_bfloat16) : NORM_RING(float);
       if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)b.smem) != cudaSuccess)
         return MOE_ERR_CUDA;
       e = launch_kernel(kern, grid, b.threads, b.smem, st, 1, a, b.depth);
     } else {
-      auto kern = bf16 ? NORM_BWD(k_block_norm_bwd, __nv_bfloat16) : NORM_BWD(k_block_norm_bwd, float);
+      // more than 12288 (bf16) or 6144 (fp32) elements: 2, or 2 to 4 vectors
+      auto kern = bf16         ? k_block_norm_bwd<__nv_bfloat16, 2>
+                  : b.vpt == 2 ? k_block_norm_bwd<float, 2>
+                  : b.vpt == 3 ? k_block_norm_bwd<float, 3>
+                               : k_block_norm_bwd<float, 4>;
       e = launch_kernel(kern, grid, b.threads, 0, st, 1, a);
     }
     MOE_TRY(cuda_rc(e));

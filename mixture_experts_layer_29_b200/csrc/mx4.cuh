@@ -163,26 +163,6 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
   return r;
 }
 
-// Two floats in one register pair, and operations on both, each rounded to nearest like a single one.
-__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack_f32x2(uint64_t p, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // The correctly rounded quotient x / d from r, the correctly rounded reciprocal of d: with t = x r it
 // is t + r (x - t d) (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990) while nothing underflows. 3 operations for a division's dozen.

@@ -228,3 +228,12 @@ def test_no_tokens(cuda_device):
     sums = [torch.full((256,), 5.0, device="cuda") for _ in range(3)]
     norm.block_norm_backward(d, e, e, e, e, w, w, w, v, v, e, e, sums[0], sums[1], sums[2], norm.workspace(d))
     assert all((x == 0).all() for x in sums)
+
+
+@pytest.mark.parametrize("T,H", [(301, 6160), (160, 8192), (151, 8208), (149, 12288), (7, 12304), (150, 16384)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("gate", ["token", "channel"])
+def test_backward_of_wide_rows_and_several_tokens_per_block(cuda_device, T, H, dtype, gate):
+    """Widths on both sides of the ones at which threads hold one vector more, or rows stop going
+    through shared memory; more tokens than the card has SMs."""
+    test_backward_is_the_formula(None, T, H, dtype, gate)
