@@ -20,7 +20,7 @@ import re
 import torch
 
 from . import abi
-from .mx4 import _F32, _U8, _check, _device, _stream, _tensor
+from .mx4 import _U8, _check, _device, _stream, _tensor, _tensors
 
 HEADER = os.path.join(os.path.dirname(abi.HEADER), "moe_norm.h")
 GATES = {"none": 0, "token": 1, "channel": 2}
@@ -32,6 +32,7 @@ class Desc(ctypes.Structure):
                 ("gate", ctypes.c_int32), ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
+_FP32 = torch.float32
 _P, _SZ = ctypes.c_void_p, ctypes.c_size_t
 _D = ctypes.POINTER(Desc)
 _SIGS = {
@@ -66,7 +67,7 @@ def make_desc(T, H, dtype="bf16", gate="none", eps=1e-5, scale=1.0) -> Desc:
     return Desc(T, H, dt, GATES[gate], eps, scale)
 
 
-_ROWS = {abi.MOE_BF16: (torch.bfloat16,), abi.MOE_FP32: (torch.float32,)}
+_ROWS = {abi.MOE_BF16: torch.bfloat16, abi.MOE_FP32: torch.float32}
 
 
 def _of_gate(d: Desc):
@@ -76,15 +77,14 @@ def _of_gate(d: Desc):
 def block_norm(d: Desc, residual, block, w_post, gate, w_pre, residual_out, normed, rstd_block=None,
                rstd_res=None, stream=None):
     """moe_block_norm; returns (residual_out, normed)."""
-    dev, rows, dt, T, H = _device(), (d.T, d.H), _ROWS.get(d.dtype, ()), (d.T,), (d.H,)
-    _check(lib().moe_block_norm(
-        ctypes.byref(d), _tensor(residual, "residual", dt, rows, dev=dev),
-        _tensor(block, "block", dt, rows, True, dev=dev), _tensor(w_post, "w_post", _F32, H, True, dev=dev),
-        _tensor(gate, "gate", _F32, _of_gate(d), True, dev=dev), _tensor(w_pre, "w_pre", _F32, H, True, dev=dev),
-        _tensor(residual_out, "residual_out", dt, rows, True, dev=dev),
-        _tensor(normed, "normed", dt, rows, True, dev=dev),
-        _tensor(rstd_block, "rstd_block", _F32, T, True, dev=dev),
-        _tensor(rstd_res, "rstd_res", _F32, T, True, dev=dev), _stream(stream, dev)), "moe_block_norm")
+    dev, rows, dt, T, H = _device(), (d.T, d.H), _ROWS.get(d.dtype), (d.T,), (d.H,)
+    if residual is None:
+        raise ValueError("residual: a tensor is needed")
+    _check(lib().moe_block_norm(ctypes.byref(d), *_tensors(
+        dev, (residual, "residual", dt, rows), (block, "block", dt, rows), (w_post, "w_post", _FP32, H),
+        (gate, "gate", _FP32, _of_gate(d)), (w_pre, "w_pre", _FP32, H), (residual_out, "residual_out", dt, rows),
+        (normed, "normed", dt, rows), (rstd_block, "rstd_block", _FP32, T), (rstd_res, "rstd_res", _FP32, T)),
+        _stream(stream, dev)), "moe_block_norm")
     return residual_out, normed
 
 
@@ -99,19 +99,17 @@ def block_norm_backward(d: Desc, d_residual_out, d_normed, residual_out, block, 
                         rstd_block, rstd_res, d_residual, d_block, d_w_post, d_gate, d_w_pre, ws,
                         stream=None):
     """moe_block_norm_backward: writes the gradients of the parts that the forward had."""
-    dev, rows, dt, T, H, G = _device(), (d.T, d.H), _ROWS.get(d.dtype, ()), (d.T,), (d.H,), _of_gate(d)
-
-    def opt(t, name, dtypes, shape):
-        return _tensor(t, name, dtypes, shape, True, dev=dev)
-
-    _check(lib().moe_block_norm_backward(
-        ctypes.byref(d), opt(d_residual_out, "d_residual_out", dt, rows), opt(d_normed, "d_normed", dt, rows),
-        opt(residual_out, "residual_out", dt, rows), opt(block, "block", dt, rows), opt(w_post, "w_post", _F32, H),
-        opt(gate, "gate", _F32, G), opt(w_pre, "w_pre", _F32, H), opt(rstd_block, "rstd_block", _F32, T),
-        opt(rstd_res, "rstd_res", _F32, T), _tensor(d_residual, "d_residual", dt, rows, dev=dev),
-        opt(d_block, "d_block", dt, rows), opt(d_w_post, "d_w_post", _F32, H), opt(d_gate, "d_gate", _F32, G),
-        opt(d_w_pre, "d_w_pre", _F32, H), _tensor(ws, "ws", _U8, dev=dev), ws.numel(), _stream(stream, dev)),
-        "moe_block_norm_backward")
+    dev, rows, dt, T, H = _device(), (d.T, d.H), _ROWS.get(d.dtype), (d.T,), (d.H,)
+    G = _of_gate(d)
+    if d_residual is None:
+        raise ValueError("d_residual: a tensor is needed")
+    _check(lib().moe_block_norm_backward(ctypes.byref(d), *_tensors(
+        dev, (d_residual_out, "d_residual_out", dt, rows), (d_normed, "d_normed", dt, rows),
+        (residual_out, "residual_out", dt, rows), (block, "block", dt, rows), (w_post, "w_post", _FP32, H),
+        (gate, "gate", _FP32, G), (w_pre, "w_pre", _FP32, H), (rstd_block, "rstd_block", _FP32, T),
+        (rstd_res, "rstd_res", _FP32, T), (d_residual, "d_residual", dt, rows), (d_block, "d_block", dt, rows),
+        (d_w_post, "d_w_post", _FP32, H), (d_gate, "d_gate", _FP32, G), (d_w_pre, "d_w_pre", _FP32, H)),
+        _tensor(ws, "ws", _U8, dev=dev), ws.numel(), _stream(stream, dev)), "moe_block_norm_backward")
 
 
 class MoEBlock:
