@@ -98,9 +98,31 @@ __device__ __forceinline__ void load_param(const float* p, int c, float (&v)[N])
   }
 }
 
+// Sum of the squares of a thread's vectors.
+template <typename T, int VPT>
+__device__ __forceinline__ float squares(const uint4 (&q)[VPT]) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    float v[Row<T>::N];
+    Row<T>::unpack(q[i], v);
+#pragma unroll
+    for (int j = 0; j < Row<T>::N; ++j) s = fmaf(v[j], v[j], s);
+  }
+  return s;
+}
+
+// A CTA's most threads (row_shape gives three and four vectors of bf16 to 256 threads only), and the CTAs
+// per SM that the registers have to allow (0: as the compiler likes). Five, not four, of 6144 columns:
+// 69.0 us instead of 72.8 for 8192 rows, six 70.6; four, not three, of 8192: 96 us instead of 111.
+template <typename T>
+constexpr int fwd_threads(int vpt) { return sizeof(T) == 2 && vpt >= 3 ? 256 : 1024; }
+template <typename T>
+constexpr int fwd_blocks(int vpt) { return sizeof(T) == 2 && vpt == 3 ? 5 : sizeof(T) == 2 && vpt == 4 ? 4 : 0; }
+
 // VPT vectors per thread, strided by the block so that a warp's loads are contiguous.
 template <typename T, int VPT>
-__global__ void __launch_bounds__(1024) k_block_norm(const FwdArgs a) {
+__global__ void __launch_bounds__(fwd_threads<T>(VPT), fwd_blocks<T>(VPT)) k_block_norm(const FwdArgs a) {
   constexpr int N = Row<T>::N;
   __shared__ float part[2][32];
   pdl_launch_dependents();
@@ -108,25 +130,21 @@ __global__ void __launch_bounds__(1024) k_block_norm(const FwdArgs a) {
   const size_t t = blockIdx.x;
   const int nvec = a.H / N;
   const uint4* res = reinterpret_cast<const uint4*>(static_cast<const T*>(a.residual) + t * a.H);
-  float r[VPT][N];
+  // the rows stay as they are in memory (12 registers for 6144 columns of bf16 on 256 threads, not 24) and
+  // are unpacked where they are used: more rows fit on an SM
+  uint4 r[VPT];
   if (a.block) {
     const uint4* blk = reinterpret_cast<const uint4*>(static_cast<const T*>(a.block) + t * a.H);
-    uint4 rq[VPT];
-    float b[VPT][N], sq = 0.f;
+    uint4 b[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      const uint4 q = v < nvec ? blk[v] : make_uint4(0, 0, 0, 0);
-      rq[i] = v < nvec ? res[v] : make_uint4(0, 0, 0, 0);
-      Row<T>::unpack(q, b[i]);
+      b[i] = v < nvec ? blk[v] : make_uint4(0, 0, 0, 0);
+      r[i] = v < nvec ? res[v] : make_uint4(0, 0, 0, 0);
     }
     float rb = 1.0f;
     if (a.w_post) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int j = 0; j < N; ++j) sq = fmaf(b[i][j], b[i][j], sq);
-      rb = rstd_of(block_sum(sq, part[0]), a.H, a.eps);
+      rb = rstd_of(block_sum(squares<T, VPT>(b), part[0]), a.H, a.eps);
       if (a.rstd_block && threadIdx.x == 0) a.rstd_block[t] = rb;
     }
     const float gt = a.scale * (a.gate == MOE_GATE_TOKEN ? a.g[t] : 1.0f);
@@ -134,44 +152,40 @@ __global__ void __launch_bounds__(1024) k_block_norm(const FwdArgs a) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      Row<T>::unpack(rq[i], r[i]);
       if (v >= nvec) continue;
-      float w[N], gc[N];
+      float w[N], gc[N], x[N], y[N];
 #pragma unroll
       for (int j = 0; j < N; ++j) w[j] = gc[j] = 1.0f;
       if (a.w_post) load_param(a.w_post, v * N, w);
       if (a.gate == MOE_GATE_CHANNEL) load_param(a.g, v * N, gc);
+      Row<T>::unpack(b[i], x);
+      Row<T>::unpack(r[i], y);
 #pragma unroll
-      for (int j = 0; j < N; ++j) r[i][j] = fmaf(gt * gc[j], b[i][j] * rb * w[j], r[i][j]);
-      const uint4 q = Row<T>::pack(r[i]);
-      out[v] = q;
-      Row<T>::unpack(q, r[i]);       // the next norm reads the stream as it is stored
+      for (int j = 0; j < N; ++j) y[j] = fmaf(gt * gc[j], x[j] * rb * w[j], y[j]);
+      r[i] = Row<T>::pack(y);        // the next norm reads the stream as it is stored
+      out[v] = r[i];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      Row<T>::unpack(v < nvec ? res[v] : make_uint4(0, 0, 0, 0), r[i]);
+      r[i] = v < nvec ? res[v] : make_uint4(0, 0, 0, 0);
     }
   }
   if (!a.w_pre) return;
-  float sq = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = 0; j < N; ++j) sq = fmaf(r[i][j], r[i][j], sq);
-  const float rr = rstd_of(block_sum(sq, part[1]), a.H, a.eps);
+  const float rr = rstd_of(block_sum(squares<T, VPT>(r), part[1]), a.H, a.eps);
   if (a.rstd_res && threadIdx.x == 0) a.rstd_res[t] = rr;
   uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.normed) + t * a.H);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     if (v >= nvec) continue;
-    float w[N];
+    float w[N], x[N];
     load_param(a.w_pre, v * N, w);
+    Row<T>::unpack(r[i], x);
 #pragma unroll
-    for (int j = 0; j < N; ++j) r[i][j] = r[i][j] * rr * w[j];
-    out[v] = Row<T>::pack(r[i]);
+    for (int j = 0; j < N; ++j) x[j] = x[j] * rr * w[j];
+    out[v] = Row<T>::pack(x);
   }
 }
 
@@ -558,7 +572,7 @@ int moe_block_norm(const moe_norm_t* n, const void* residual, const void* block,
             rstd_block, rstd_res};
   const bool bf16 = n->dtype == MOE_BF16;
   // few tokens: many threads per row, for the shortest way through; more: 256, so that an SM has
-  // several rows under way (8192 x 6144 bf16: 108, 82, 73, 75 us with 768, 384, 256, 192 threads)
+  // several rows under way (8192 x 6144 bf16, before: 108, 82, 73, 75 us with 768, 384, 256, 192 threads)
   int vpt, threads;
   row_shape(n->H / (bf16 ? 8 : 4), n->T > 2 * dev.sm_count ? 256 : 1024, &vpt, &threads);
 #define NORM_VPT(T) \
