@@ -13,8 +13,9 @@
  *                  holds an infinity or a NaN gets b = 255, and all its values are NaN.
  *   MOE_MX4_NVFP4  blocks of 16, scale byte e4m3: s = e4m3(|x| / (6 t)) (at most 448), element
  *                  e2m1(x / (s t)), value element * s * t, with t the tensor's fp32 factor
- *                  (1 when no factor is given; positive, from 2^-100 to 2^100). A block with s = 0 is all zeros. A block with
- *                  an infinity or a NaN gets the e4m3 NaN, and all its values are NaN.
+ *                  (1 when no factor is given; positive, from 2^-100 to 2^100). A block with
+ *                  s = 0 is all zeros. A block with an infinity or a NaN gets the e4m3 NaN,
+ *                  and all its values are NaN.
  * The fp32 operations round to nearest: 6 t, |x| / (6 t), s t and x / (s t), one each.
  *
  * Rows and groups. A 4-bit matrix has `rows` rows of K elements in `groups` groups, group g
