@@ -230,7 +230,8 @@ def test_no_tokens(cuda_device):
     assert all((x == 0).all() for x in sums)
 
 
-@pytest.mark.parametrize("T,H", [(301, 6160), (160, 8192), (151, 8208), (149, 12288), (7, 12304), (150, 16384)])
+@pytest.mark.parametrize("T,H", [(301, 6160), (160, 8192), (151, 8208), (149, 12288), (7, 12304), (150, 16384),
+                                 (2047, 2048), (2048, 2048), (2100, 1040), (2050, 4096), (2049, 3344)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("gate", ["token", "channel"])
 def test_backward_of_wide_rows_and_several_tokens_per_block(cuda_device, T, H, dtype, gate):
