@@ -5,8 +5,8 @@
 //   h[r, i] = q(silu(A Wg^T) * (A Wu^T))             (the FFN's gate and up)
 //
 // The weights are the M side of the MMA (128 rows), a group's rows the N side. A decode step has
-// a few rows per group and then is bound by streaming the weights, so the side that is padded to
-// 128 is the one that has the rows, and N shrinks with the group to 16. Each tile holds two
+// a few rows per group and then is bound by streaming the weights, so it is the weights' side that
+// comes in blocks of 128, and N shrinks with the group to 16. Each tile holds two
 // weight blocks of 128 rows, which share the tile's rows: the gate and up rows of the same 128
 // channels of h, or 256 outputs of a plain product. TMEM lane = output channel, column = row.
 //
@@ -19,7 +19,8 @@
 //    of which each CTA holds. An e2m1 MMA of one CTA reads both operands from its shared memory
 //    at about the rate that memory has (107 bytes a cycle at N = 192 besides what TMA writes); in
 //    a pair each CTA reads half of the rows. Two accumulators let the epilogue of a tile overlap
-//    the MMAs of the next.
+//    the MMAs of the next. Of 352 us for 32768 x 4096 x 6144 (4.7 PFLOP/s) the loads alone take 274,
+//    59 bytes a cycle into each SM, and the MMAs alone some 255: the two meet in shared memory.
 // Warps, one CTA:
 //   0           TMA producer: per stage of K = 256 elements (128 bytes, 128-byte swizzle) the
 //               weight boxes, the tile's rows in a few boxes, and the block scales as plain bulk
