@@ -380,3 +380,78 @@ def test_rows_aligned_to_16_bytes_only(cuda_device, fmt, dtype, K, shift, pad):
     out = torch.empty(37, K, dtype=torch.float32, device="cuda")
     mx4.dequantize(m, out)
     assert torch.equal(out.double(), value)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_offsets_past_32_bits(cuda_device, fmt):
+    """More than 2^32 elements in the rows, 2^31 bytes in their codes and 2^31 elements in a product: the
+    last rows are what a small matrix of them gives, a weight's last group what that group alone gives."""
+    rows, K, N, last = 706_000, 6144, 128, 200
+    t = factor(fmt)
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    x[-last:] = torch.randn(last, K, device="cuda", generator=gen(1)).to(torch.bfloat16)
+    a, b = mx4.allocate(fmt, rows, K, tensor_scale=t), mx4.allocate(fmt, last, K, tensor_scale=t)
+    mx4.quantize(x, a)
+    mx4.quantize(x[-last:], b)
+    assert torch.equal(a.codes[-last:], b.codes)
+    back = torch.empty(last, K, dtype=torch.bfloat16, device="cuda")
+    mx4.dequantize(a, x)
+    mx4.dequantize(b, back)
+    assert torch.equal(x[-last:], back) and not bool(x[:-last].any())
+    del x
+    w = mx4.quantize_weight(torch.randn(1, N, K, device="cuda", generator=gen(2)).clamp(-6.0, 6.0), fmt)
+    ws = mx4.gemm_workspace()
+    big, small = (torch.empty(n, N, device="cuda") for n in (rows, last))
+    mx4.grouped_gemm(a, w, big, ws)
+    mx4.grouped_gemm(b, w, small, ws)
+    # the same sums at another place of a tile: each off by 96 steps of sum |a| |w| at most
+    mag = back.double().abs().sum(1, keepdim=True) * 6.5          # |w| <= 6, or what its scale rounds that to
+    assert bool(((big[-last:] - small).double().abs() <= 2 * mag * 96 * STEP).all())
+    assert not bool(big[:-last].any())
+    del a, big
+    # outputs of more than 2^31 elements
+    rows, K, N = 530_000, 128, 4096 + 8
+    a, b = mx4.allocate(fmt, rows, K, tensor_scale=t), mx4.allocate(fmt, last, K, tensor_scale=t)
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    x[-last:] = 1.5
+    mx4.quantize(x, a)
+    mx4.quantize(x[-last:], b)
+    w = mx4.quantize_weight(torch.randint(-2, 3, (1, N, K), device="cuda", generator=gen(3)).float(), fmt)
+    big, small = (torch.empty(n, N, dtype=torch.bfloat16, device="cuda") for n in (rows, last))
+    mx4.grouped_gemm(a, w, big, ws)
+    mx4.grouped_gemm(b, w, small, ws)
+    assert torch.equal(big[-last:], small) and not bool(big[:-last].any())
+    assert abi.read_device_status(ws) == 0
+    del a, x, big
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("counts", [3, 200])
+def test_weights_past_32_bits(cuda_device, fmt, counts):
+    """The weights of 400 experts, 5 GB of codes, by both kernels."""
+    groups, N, K = 400, 4096, 6144
+    codes = torch.randint(0, 256, (groups, N, K // 2), device="cuda", generator=gen(4), dtype=torch.uint8)
+    byte = torch.full((groups, N, K // ref.BLOCK[fmt]), 127 if fmt == "mxfp4" else 56, device="cuda", dtype=torch.uint8)
+    w = mx4.from_checkpoint(fmt, codes, byte)
+    off = [0] * (groups - 1) + [counts, 2 * counts]             # the last two groups have rows
+    rows = 2 * counts if counts < 64 else 64 * groups + 1       # as many as there may be: one CTA, or pairs
+    m = mx4.allocate(fmt, rows, K, groups, dev(off))
+    x = torch.randint(-4, 5, (rows, K), device="cuda", generator=gen(5)).to(torch.bfloat16)
+    x[:, ::16] = 4.0                                            # codes are exact: scale 1 (2/3 in NVFP4: rounded)
+    mx4.quantize(x, m)
+    value = torch.zeros(rows, K, device="cuda")
+    mx4.dequantize(m, value)
+    out = torch.empty(rows, N, device="cuda")
+    ws = mx4.gemm_workspace()
+    mx4.grouped_gemm(m, w, out, ws)
+    for g in (groups - 2, groups - 1):
+        c = torch.stack([codes[g] & 15, codes[g] >> 4], -1).flatten(-2)
+        v = ref.GRID.cuda()[(c & 7).long()]
+        v = torch.where(c > 7, -v, v)
+        r = slice(off[g], off[g + 1])
+        y, mag = value[r].double() @ v.T, value[r].double().abs() @ v.abs().T
+        assert bool(((out[r].double() - y).abs() <= mag * 96 * STEP).all())
+    assert abi.read_device_status(ws) == 0
+    del codes, byte, w
+    torch.cuda.empty_cache()

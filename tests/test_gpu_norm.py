@@ -238,3 +238,31 @@ def test_backward_of_wide_rows_and_several_tokens_per_block(cuda_device, T, H, d
     """Widths on both sides of the ones at which threads hold one vector more, or rows stop going
     through shared memory; more tokens than the card has SMs."""
     test_backward_is_the_formula(None, T, H, dtype, gate)
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """More than 2^31 elements: the last tokens' rows are those of a small batch of them."""
+    T, H, last = 351_000, 6144, 400          # more than two tokens per SM: the same CTAs for both
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.randn(H, device="cuda", generator=g) + 1.0
+    z = lambda: torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")      # noqa: E731
+    ins = [z() for _ in range(4)]                                           # residual, block, their gradients
+    for x in ins:
+        x[-last:] = torch.randn(last, H, device="cuda", generator=g).to(torch.bfloat16)
+    results = []
+    for n in (T, last):
+        d = norm.make_desc(n, H, "bf16", "none", EPS, 0.5)
+        res, blk, d_res, d_norm = (x[-n:].contiguous() for x in ins)
+        e = lambda: torch.empty(n, H, dtype=torch.bfloat16, device="cuda")  # noqa: E731, B023
+        v = lambda: torch.empty(n, device="cuda")                           # noqa: E731, B023
+        out, normed, rb, rr, dr, db = e(), e(), v(), v(), e(), e()
+        norm.block_norm(d, res, blk, w, None, w, out, normed, rb, rr)
+        dw, dp = torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+        norm.block_norm_backward(d, d_res, d_norm, out, blk, w, None, w, rb, rr, dr, db, dw, None, dp, norm.workspace(d))
+        results.append([x[-last:].clone() for x in (out, normed, dr, db)] + [bool(x[:-last].any()) for x in (out, normed, dr, db)])
+        del res, blk, d_res, d_norm, out, normed, dr, db
+    for a, b in zip(results[0][:4], results[1][:4]):
+        assert torch.equal(a, b)
+    assert not any(results[0][4:])
+    del ins
+    torch.cuda.empty_cache()
