@@ -170,8 +170,9 @@ __device__ __forceinline__ float quotient(float x, float d, float r) {
   const float t = __fmul_rn(x, r);
   return __fmaf_rn(r, __fmaf_rn(-t, d, x), t);
 }
-// d for which quotient() is good: an x so small beside it that x - t d underflows has a quotient
-// below 2^-40, which rounds to 0 on every grid here.
+// d for which quotient() is good while |x / d| is below 2^66 or so: an x so small beside d that x - t d
+// underflows has a quotient below 2^-40, which rounds to 0 on every grid here. (A larger x would make
+// x r infinite, and the correction of that a NaN.)
 __device__ __forceinline__ bool quotient_ok(float d) { return d >= 0x1p-60f && d <= 0x1p60f; }
 
 // t of an NVFP4 matrix with what its scales are made with.
@@ -192,7 +193,9 @@ __device__ __forceinline__ uint32_t mx4_scale(float amax, const Mx4Factor& f, fl
   by = 0.f;
   if (NV) {
     if (bits >= 0x7F800000u) return 0x7Fu;
-    const uint32_t s = e4m3(quotient_ok(f.six) ? quotient(amax, f.six, f.r) : __fdiv_rn(amax, f.six));
+    // 448 is the largest scale: every quotient from there on gives it, the quotients' own range ends nowhere
+    const float a = fminf(amax, 512.0f * f.six);
+    const uint32_t s = e4m3(quotient_ok(f.six) ? quotient(a, f.six, f.r) : __fdiv_rn(a, f.six));
     by = __fmul_rn(e4m3_value(s), f.t);
     return s;
   }
@@ -202,9 +205,9 @@ __device__ __forceinline__ uint32_t mx4_scale(float amax, const Mx4Factor& f, fl
   by = __uint_as_float((254u - b) << 23);
   return b;
 }
-// The codes of 8 elements of a block (the first in the low bits).
+// The codes of 8 elements of a block (the first in the low bits) whose largest magnitude is amax.
 template <bool NV>
-__device__ __forceinline__ uint32_t mx4_codes(const float (&x)[8], float by) {
+__device__ __forceinline__ uint32_t mx4_codes(const float (&x)[8], float by, float amax) {
   float q[8];
   // a block of zeros must not end in the divisions (17081 rows of 768, a quarter of whose lanes have
   // none, took 22 us instead of 10)
@@ -213,7 +216,7 @@ __device__ __forceinline__ uint32_t mx4_codes(const float (&x)[8], float by) {
     const uint64_t s = pack_f32x2(d, d);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) unpack_f32x2(mul_f32x2(pack_f32x2(x[i], x[i + 1]), s), q[i], q[i + 1]);
-  } else if (quotient_ok(d)) {
+  } else if (quotient_ok(d) && amax <= 0x1p66f * d) {
     const float r = __frcp_rn(d);
     const uint64_t r2 = pack_f32x2(r, r), minus = pack_f32x2(-d, -d);
 #pragma unroll
@@ -223,7 +226,7 @@ __device__ __forceinline__ uint32_t mx4_codes(const float (&x)[8], float by) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], d);
+    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], d);   // infinite past the range: at most 6
   }
   const uint32_t c = e2m1x8(q);
   return by != 0.f ? c : 0u;

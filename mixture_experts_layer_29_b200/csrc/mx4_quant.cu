@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_mx4_quantize(const QuantArgs 
     if (kLanes == 2) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
     float by;
     const uint32_t byte = mx4_scale<NV>(top, f, by);
-    code[s] = make_uint2(mx4_codes<NV>(a, by), mx4_codes<NV>(b, by));
+    code[s] = make_uint2(mx4_codes<NV>(a, by, top), mx4_codes<NV>(b, by, top));
     // the four scales of one piece's row, gathered from its 8 (4) lanes into a word
     uint32_t w = byte << (8 * ((lane / kLanes) & 3));
     w |= __shfl_xor_sync(0xffffffffu, w, kLanes);
