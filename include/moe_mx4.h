@@ -103,7 +103,10 @@ int moe_mx4_grouped_gemm(const moe_mx4_t* a, const moe_mx4_t* w, void* out, int3
 /* Grouped SwiGLU FFN on 4-bit experts (report §2.4: intermediate I per expert):
  *   h = q(silu(A Wg^T) * (A Wu^T)),  y = h Wd^T
  * with q() the rounding of h to a's format (h_factor: its t, device fp32 [1] or NULL; NULL
- * for MXFP4). silu and the product are fp32; h never exists in more than 4 bits.
+ * for MXFP4) by the operations above. silu and the product are fp32, good to a few units in the
+ * last place, and the sums A Wg^T, A Wu^T go in the tensor cores' order: an h that lies that
+ * near the middle of two 4-bit numbers, or its block's |h| / (6 t) that of two scales, may go
+ * either way. h never exists in more than 4 bits.
  *   a          [rows, H], ragged or uniform groups
  *   w_gate_up  uniform groups of 2I rows of H elements: rows [0, I) gate, [I, 2I) up
  *   w_down     uniform groups of H rows of I elements

@@ -205,30 +205,32 @@ __device__ __forceinline__ uint32_t mx4_scale(float amax, const Mx4Factor& f, fl
   by = __uint_as_float((254u - b) << 23);
   return b;
 }
-// The codes of 8 elements of a block (the first in the low bits) whose largest magnitude is amax.
-template <bool NV>
-__device__ __forceinline__ uint32_t mx4_codes(const float (&x)[8], float by, float amax) {
-  float q[8];
+// The codes of 4 or 8 elements of a block (the first in the low bits) whose largest magnitude is amax.
+template <bool NV, int N>
+__device__ __forceinline__ uint32_t mx4_codes(const float (&x)[N], float by, float amax) {
+  float q[N];
   // a block of zeros must not end in the divisions (17081 rows of 768, a quarter of whose lanes have
   // none, took 22 us instead of 10)
   const float d = by != 0.f ? by : 1.0f;
   if (!NV) {
     const uint64_t s = pack_f32x2(d, d);
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) unpack_f32x2(mul_f32x2(pack_f32x2(x[i], x[i + 1]), s), q[i], q[i + 1]);
+    for (int i = 0; i < N; i += 2) unpack_f32x2(mul_f32x2(pack_f32x2(x[i], x[i + 1]), s), q[i], q[i + 1]);
   } else if (quotient_ok(d) && amax <= 0x1p66f * d) {
     const float r = __frcp_rn(d);
     const uint64_t r2 = pack_f32x2(r, r), minus = pack_f32x2(-d, -d);
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {       // quotient() of two elements at once
+    for (int i = 0; i < N; i += 2) {       // quotient() of two elements at once
       const uint64_t v = pack_f32x2(x[i], x[i + 1]), n = mul_f32x2(v, r2);
       unpack_f32x2(fma_f32x2(r2, fma_f32x2(n, minus, v), n), q[i], q[i + 1]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], d);   // infinite past the range: at most 6
+    for (int i = 0; i < N; ++i) q[i] = __fdiv_rn(x[i], d);   // infinite past the range: at most 6
   }
-  const uint32_t c = e2m1x8(q);
+  uint32_t c;
+  if constexpr (N == 8) c = e2m1x8(q);
+  else c = e2m1x2(q[0], q[1]) | e2m1x2(q[2], q[3]) << 8;
   return by != 0.f ? c : 0u;
 }
 
