@@ -246,8 +246,16 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_wait() {
+// Waits for this warp's loads from TMEM, and names what they loaded: the compiler takes a load's registers
+// for written where the load stands, so without their names here it may move a use above the wait.
+template <int... N>
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&...v)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  const auto tie = [](uint32_t* r, int n) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) asm volatile("" : "+r"(r[i])::"memory");
+  };
+  (tie(v, N), ...);
 }
 
 // --- CTA pairs (cluster of 2, tcgen05 cta_group::2) ----------------------------------------

@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 128 * h; c < 128 * h + 128; c += 32) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(tbase + c, v);
-        tmem_ld_wait();
+        tmem_ld_wait_for(v);
         const int col = t.nt * BN + c;
         if (g.mode == kDH) {
           if (row < row_end && col < g.n_valid) {
@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t v[2][32];
         tmem_ld_32x32b_x32(tbase + 64 * b, v[0]);
         tmem_ld_32x32b_x32(tbase + 64 * b + 32, v[1]);
-        tmem_ld_wait();
+        tmem_ld_wait_for(v[0], v[1]);
         if (b == 1) {
           tc_fence_before();
           __syncwarp();

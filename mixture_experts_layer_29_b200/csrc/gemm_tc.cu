@@ -173,7 +173,7 @@ __device__ __forceinline__ void epi_gateup_chunk(const GemmArgs& g, const Tile& 
   uint32_t gr[32], ur[32];
   tmem_ld_32x32b_x32(tbase + gcol, gr);
   tmem_ld_32x32b_x32(tbase + ucol, ur);
-  tmem_ld_wait();
+  tmem_ld_wait_for(gr, ur);
   if (row >= t.row_end) return;
   if (g.gu_raw) {
     // G to columns [nt*128 + oc, +32) and U to I + that of the row (ld_out = 2I)
@@ -238,7 +238,7 @@ __device__ __forceinline__ void epi_down_chunk(const GemmArgs& g, const Tile& t,
                                                float (*stg)[20], int lane) {
   uint32_t yr[32];
   tmem_ld_32x32b_x32(tbase + tcol, yr);
-  tmem_ld_wait();
+  tmem_ld_wait_for(yr);
   const int col = t.nt * BN + oc;
   if (g.mode == kDownStore) {
     // this lane's row as 64 bytes of bf16 into the staging row, then 16 bytes per lane of
@@ -312,7 +312,7 @@ __device__ __forceinline__ void epi_dh_chunk(const GemmArgs& g, const Tile& t, u
                                              int row, int tcol, int oc) {
   uint32_t v[32];
   tmem_ld_32x32b_x32(tbase + tcol, v);
-  tmem_ld_wait();
+  tmem_ld_wait_for(v);
   const int col = t.nt * BN + oc;
   if (row >= t.row_end || col >= g.n_valid) return;
   const int I = g.n_valid;
@@ -346,7 +346,7 @@ __device__ __forceinline__ void epi_dx_chunk(const GemmArgs& g, const Tile& t, u
                                              int lane) {
   uint32_t v[32];
   tmem_ld_32x32b_x32(tbase + tcol, v);
-  tmem_ld_wait();
+  tmem_ld_wait_for(v);
   float* out = static_cast<float*>(g.out);
   const int row_base = row - lane;
 #pragma unroll
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < NH; c += 32) {
             uint32_t v[32];
             tmem_ld_32x32b_x32(tbase + NH * half + c, v);
-            tmem_ld_wait();
+            tmem_ld_wait_for(v);
 #pragma unroll
             for (int i = 0; i < 32; ++i) sum[c + i] = __fadd_rn(sum[c + i], __uint_as_float(v[i]));
           }
@@ -829,7 +829,7 @@ __device__ __forceinline__ void epilogue_swap(const GemmArgs& g, const Tile& t, 
     if (16 * h < ncol) {
       uint32_t v[16];
       tmem_ld_32x32b_x16(tbase + (uint32_t)(c0 + 16 * h), v);
-      tmem_ld_wait();
+      tmem_ld_wait_for(v);
 #pragma unroll
       for (int j = 0; j < 16; ++j) S[(16 * h + j) * SS + 32 * q + lane] = __uint_as_float(v[j]);
     }

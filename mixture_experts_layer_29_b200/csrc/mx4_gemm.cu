@@ -302,14 +302,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
 
-// tmem_ld_wait, with what was loaded: no use of it moves above the wait.
-template <int N>
-__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[N]) {
-  tmem_ld_wait();
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i])::"memory");
-}
-
 // Whether the phase of the given parity is over, without waiting for it.
 __device__ __forceinline__ uint32_t mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -722,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t v[2][16];
         tmem_ld_32x32b_x16(base + c, v[0]);
         tmem_ld_32x32b_x16(base + NT + c, v[1]);
-        tmem_ld_wait();
+        tmem_ld_wait_for(v[0], v[1]);
 #pragma unroll
         for (int e = 0; e < 16; e += 8) {
           float x[8];
