@@ -527,6 +527,7 @@ void row_shape(int nvec, int most, int* vpt, int* threads) {
 // The backward's CTAs. With the ring, for rows of up to 2 x 768 vectors of which two tokens' fit: up to 768
 // threads of one or two vectors, as many CTAs as make up 768 threads per SM. Without (depth 0): up to 1024
 // threads, one CTA per SM.
+constexpr size_t kRingBytes = 200 * 1024;      // of an SM's rings
 struct BwdShape {
   int vpt, threads, per_sm, depth;
   size_t smem;
@@ -548,7 +549,7 @@ BwdShape bwd_shape(const moe_norm_t& n) {
     const int per_sm = (esz == 2 ? 512 : kRingThreads) / threads;
     if (per_sm * threads >= b.per_sm * b.threads) b.vpt = vpt, b.threads = threads, b.per_sm = per_sm;
   }
-  b.depth = (int)min((size_t)kMaxDepth, (size_t)200 * 1024 / b.per_sm / token);
+  b.depth = (int)min((size_t)kMaxDepth, kRingBytes / b.per_sm / token);
   if (b.depth < 2 || !narrow) b.depth = 0;
   b.smem = b.depth * token;
   return b;
@@ -646,7 +647,9 @@ int moe_block_norm_backward(const moe_norm_t* n, const void* d_residual_out, con
    : b.threads * b.per_sm <= ROOM && b.threads <= 512 ? k_block_norm_bwd_ring<T, 2, 512> \
                                 : k_block_norm_bwd_ring<T, 2, kRingThreads>)
       auto kern = bf16 ? NORM_RING(__nv_bfloat16, 512) : NORM_RING(float, 704);
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)b.smem) != cudaSuccess)
+      // the same value for every shape: the limit is the kernel's, and a call from another thread may set it
+      // between this call's setting and its launch
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes) != cudaSuccess)
         return MOE_ERR_CUDA;
       e = launch_kernel(kern, grid, b.threads, b.smem, st, 1, a, b.depth);
     } else {
