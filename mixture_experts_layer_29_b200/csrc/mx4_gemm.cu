@@ -383,6 +383,26 @@ __device__ __forceinline__ uint4 turn_to_bf16(const float (&v)[8], float f, int 
   return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
+// The product of the two factors, each from 2^-100 to 2^100: f, after a multiplication of the sums by `by`,
+// a power of two that is 1 unless the product itself leaves fp32's range. A sum other than 0 has a magnitude
+// from 2^-20 on: by f and `by` it becomes infinite, or smaller than any number, only where the result is.
+struct Factors {
+  float f, by;
+};
+template <bool NV>
+__device__ __forceinline__ Factors factors(const Args& g, float a, int group) {
+  if (!NV || !g.w_factor) return Factors{a, 1.0f};
+  const float w = g.w_factor[g.w_factor_per_group ? group : 0], f = a * w;
+  if (f >= 0x1p-126f && f <= 0x1p126f) return Factors{f, 1.0f};
+  return f > 1.0f ? Factors{a * 0x1p-100f * w, 0x1p100f} : Factors{a * 0x1p100f * w, 0x1p-100f};
+}
+// The sums as loaded, times `by`.
+template <int N>
+__device__ __forceinline__ void prescale(uint32_t (&v)[N], float by) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * by);
+}
+
 // silu(x) u = x / (1 + e^-x) u, in that order, each step to fp32's last place or two: h goes on to 4 bits,
 // where the last places decide which way a value goes that lies half way between two numbers. (With __expf
 // and __fdividef up to 16 of the 33 million elements of 16384 rows' h went another way than by fp32's own
@@ -704,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Mx4Factor hf = mx4_factor(NV && MODE == kSwiglu && g.h_factor ? *g.h_factor : 1.0f);
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
       const Tile t = decode(s, g, tile, NT);
-      const float f = NV && g.w_factor ? af * g.w_factor[g.w_factor_per_group ? t.g : 0] : af;
+      const auto [f, by] = factors<NV>(g, af, t.g);
       if (!warp_wait(&s.tfull[acc], acc_phase, abort_flag)) break;
       tc_fence_after();
       const uint32_t base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 2 * NT);
@@ -715,6 +735,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_32x32b_x16(base + c, v[0]);
         tmem_ld_32x32b_x16(base + NT + c, v[1]);
         tmem_ld_wait_for(v[0], v[1]);
+        if (NV && by != 1.0f) {
+          prescale(v[0], by);
+          prescale(v[1], by);
+        }
 #pragma unroll
         for (int e = 0; e < 16; e += 8) {
           float x[8];
@@ -1068,7 +1092,7 @@ __global__ void __launch_bounds__(pair_threads(MODE), 1)
     const Mx4Factor hf = mx4_factor(NV && MODE == kSwiglu && g.h_factor ? *g.h_factor : 1.0f);
     for (int tile = cluster; tile < total; tile += nclusters) {
       const Tile t = decode(s, g, tile, NT);
-      const float f = NV && g.w_factor ? af * g.w_factor[g.w_factor_per_group ? t.g : 0] : af;
+      const auto [f, by] = factors<NV>(g, af, t.g);
       int w_ok = warp_wait(&s.tfull[acc], acc_phase, abort_flag) ? 1 : 0;
       // all four warps of a range leave together: they meet at its barrier
       if (MODE == kSwiglu) {
@@ -1085,6 +1109,7 @@ __global__ void __launch_bounds__(pair_threads(MODE), 1)
         uint32_t v[16];
         tmem_ld_32x32b_x16(base + c, v);
         tmem_ld_wait_for(v);
+        if (NV && by != 1.0f) prescale(v, by);
         if constexpr (MODE == kSwiglu) {
 #pragma unroll
           for (int e = 0; e < 16; e += 8) {

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import mx4_reference as ref
-from mixture_experts_layer_29_b200 import mx4
+from mixture_experts_layer_29_b200 import abi, mx4
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,52 @@ def test_finite_blocks_saturate(cuda_device, fmt, exponent, dtype):
     assert torch.equal(m.codes, ref.pack(code))
     out = mx4.dequantize(m, torch.empty(rows, K, device="cuda"))
     assert torch.equal(out, value.float())
+
+
+def exact_codes(shape, seed):
+    """NVFP4 codes and scale bytes 2^-6 to 2^-4, whose products' sums fp32 holds, and their values."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    code = torch.randint(0, 16, shape, device="cuda", generator=g).to(torch.uint8)
+    e = torch.randint(-6, -3, (*shape[:-1], shape[-1] // 16), device="cuda", generator=g)
+    v = ref.GRID.cuda()[(code & 7).long()] * torch.where(code > 7, -1.0, 1.0)
+    return code, ((e + 7) << 3).to(torch.uint8), v * torch.exp2(e.double()).repeat_interleave(16, -1)
+
+
+@pytest.mark.parametrize("ea,ew", [(64, 66), (100, 100), (100, 27), (-64, -64), (-100, -27), (-100, -100), (-63, -60), (100, -100)])
+@pytest.mark.parametrize("rows", [40, 200])                     # one CTA per tile, and CTA pairs
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_factors_whose_product_leaves_the_float_range(cuda_device, ea, ew, rows, dtype):
+    """y = t_a t_w sum: the sums of zeros stay zero, others are what float64 gives, rounded, infinite
+    only where that is."""
+    N, K = 136, 256
+    code, byte, a = exact_codes((rows, K), 1)
+    wc, wb, w = exact_codes((1, N, K), 2)
+    code[3], a[3] = 0, 0.0
+    ta, tw = (torch.full((1,), m * 2.0 ** e, device="cuda") for m, e in ((1.0, ea), (1.0 if ew == 100 else 1.37, ew)))
+    m = mx4.allocate("nvfp4", rows, K, tensor_scale=ta)
+    m.codes.copy_(ref.pack(code))
+    m.scales[ref.scale_index([0, rows], K, "nvfp4", "cuda")] = byte
+    ws = mx4.gemm_workspace()
+    y = mx4.grouped_gemm(m, mx4.from_checkpoint("nvfp4", ref.pack(wc), wb, tw), torch.empty(rows, N, device="cuda", dtype=dtype), ws)
+    want = (a @ w[0].T) * ta.double() * tw.double()
+    assert abi.read_device_status(ws) == 0 and bool((y[3] == 0).all())
+    # the factors' product, the multiplication by it, the output's rounding; the smallest denormal's step
+    tol = want.abs() * 2.0 ** -23 + 2.0 ** -149
+    if dtype == torch.bfloat16:
+        tol = tol * (1 + 2.0 ** -8) + want.abs() * 2.0 ** -8 + 2.0 ** -134
+    big = want.abs() > torch.finfo(dtype).max * (1 - 2.0 ** -8)
+    assert bool((y.double() - want).abs()[~big].le(tol[~big]).all())
+    assert torch.equal(y[big].sign().double(), want[big].sign()) and bool((y[big].abs() >= torch.finfo(dtype).max * (1 - 2.0 ** -7)).all())
+
+
+@pytest.mark.parametrize("rows", [40, 200])
+def test_ffn_of_zero_rows_with_the_largest_factors(cuda_device, rows):
+    H, inter = 128, 256
+    t = torch.full((1,), 2.0 ** 100, device="cuda")
+    x = torch.zeros(rows, H, device="cuda")
+    a = mx4.quantize(x, mx4.allocate("nvfp4", rows, H, tensor_scale=t))
+    w = mx4.quantize_weight(torch.ones(1, 2 * inter, H, device="cuda"), "nvfp4", t)
+    d = mx4.quantize_weight(torch.ones(1, H, inter, device="cuda"), "nvfp4", t)
+    ws = mx4.ffn_workspace(a, w)
+    y = mx4.grouped_ffn(a, w, d, torch.empty(rows, H, device="cuda"), ws, t)
+    assert bool((y == 0).all()) and abi.read_device_status(ws) == 0
