@@ -23,7 +23,8 @@
  *   ragged   o = `offsets`, device int32 [groups + 1], ascending from 0, o_groups <= rows.
  *            Rows from o_groups on belong to no group: no call writes them, and what they hold
  *            has no effect. (The products report offsets that are not so as
- *            MOE_ERR_DEVICE_CHECK and keep to the buffers; their outputs are then undefined.)
+ *            MOE_ERR_DEVICE_CHECK and keep to the buffers; their outputs are then undefined,
+ *            and not written where the offsets are out of order.)
  *   uniform  `offsets` NULL: o_g = g * group_rows, groups * group_rows == rows.
  *
  * Layout. codes: [rows, K / 2] bytes, the even element of a pair in the low half. scales: the

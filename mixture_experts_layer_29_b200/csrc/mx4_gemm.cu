@@ -496,8 +496,9 @@ __device__ __forceinline__ void epi_store_bf16(const Args& a, const Tile& t, int
   }
 }
 
-// The tables of the groups' rows and row tiles, by every thread of the CTA. Offsets outside the matrix
-// (or, below, out of order) leave no row outside of it: they are clamped and reported.
+// The tables of the groups' rows and row tiles, by every thread of the CTA. Offsets outside the matrix are
+// clamped and reported; where some are out of order there are no tiles at all (their rows, counted several
+// times, would have no bound that the tiles' indices are made for).
 template <class S>
 __device__ __forceinline__ void build_table(S& s, const Args& g, int NT) {
   for (int i = threadIdx.x; i <= g.a.groups; i += blockDim.x) {
@@ -511,14 +512,20 @@ __device__ __forceinline__ void build_table(S& s, const Args& g, int NT) {
     const int lane = threadIdx.x & 31;
     const int per = (g.a.groups + 31) / 32;
     const int b = lane * per;
+    bool ordered = true;
     auto tiles_of = [&](int e) {
       const int n = s.offs[e + 1] - s.offs[e];
-      if (n < 0) set_status(g.status, MOE_ERR_DEVICE_CHECK);
+      if (n < 0) ordered = false;
       return n > 0 ? (n + NT - 1) / NT : 0;
     };
     int local = 0;
     for (int i = 0; i < per; ++i)
       if (b + i < g.a.groups) local += tiles_of(b + i);
+    if (!__all_sync(0xffffffffu, ordered)) {
+      set_status(g.status, MOE_ERR_DEVICE_CHECK);
+      if (lane == 31) s.toff[g.a.groups] = 0;
+      return;
+    }
     const int inc = warp_inclusive_scan(local);
     int run = inc - local;
     for (int i = 0; i < per; ++i)
