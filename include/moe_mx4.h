@@ -114,7 +114,8 @@ int moe_mx4_grouped_gemm(const moe_mx4_t* a, const moe_mx4_t* w, void* out, int3
  *   out        store (perm_token NULL): device [a.rows, H] `dtype`, out[r] = y[r].
  *              fused combine: device fp32 [*, H] (dtype MOE_FP32), out[perm_token[r]] +=
  *              scale * row_gate[r] * y[r] by fp32 atomic adds (moe_permute's perm_token and
- *              row_gate; the summation order, hence the last bits, vary run to run)
+ *              row_gate, which go together, [a.rows] each; the summation order, hence the last
+ *              bits, vary run to run)
  *   ws         device, >= moe_mx4_ffn_workspace_size bytes, zeroed before first use (status
  *              word, h). Calls that run at once need one each.
  * I is a multiple of 128. */

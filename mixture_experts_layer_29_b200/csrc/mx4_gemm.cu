@@ -1366,6 +1366,8 @@ int moe_mx4_grouped_ffn(const moe_mx4_t* a, const moe_mx4_t* w_gate_up, const mo
   if (perm_token) {
     if (dtype != MOE_FP32) return MOE_ERR_INVALID_ARG;
     MOE_TRY(check_ptrs({perm_token, row_gate}));
+  } else if (row_gate) {
+    return MOE_ERR_INVALID_ARG;
   }
   if (a->rows == 0) return MOE_OK;
   MOE_TRY(check_ptrs({a->codes, a->scales, w_gate_up->codes, w_gate_up->scales, w_down->codes, w_down->scales, out}));

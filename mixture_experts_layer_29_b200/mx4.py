@@ -85,8 +85,9 @@ def _check(rc: int, where: str):
         raise abi.MoEError(rc, where)
 
 
-def _tensor(t, name, dtypes, shape=None, optional=False, contiguous=True, dev=None):
-    """Checks one tensor argument and returns its address (None for an absent optional one)."""
+def _tensor(t, name, dtypes, shape=None, optional=False, contiguous=True, dev=None, least=0):
+    """Checks one tensor argument (of at least `least` elements) and returns its address (None for an
+    absent optional one)."""
     if t is None and optional:
         return None
     if not isinstance(t, torch.Tensor):
@@ -95,6 +96,8 @@ def _tensor(t, name, dtypes, shape=None, optional=False, contiguous=True, dev=No
         raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.numel() < least:
+        raise ValueError(f"{name}: {t.numel()} elements, {least} are needed")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
     if t.get_device() != (_device() if dev is None else dev) or not t.is_cuda:
@@ -255,13 +258,17 @@ def grouped_ffn(a: Matrix, w_gate_up: Matrix, w_down: Matrix, out, ws, h_scale=N
                 row_gate=None, scale=1.0, stream=None):
     """The grouped SwiGLU FFN on 4-bit experts. Without perm_token: out [a.rows, H] bf16 or
     fp32, one row each. With it (fused combine): out fp32 [tokens, H], to which
-    scale * row_gate[r] * y[r] is added at perm_token[r]."""
+    scale * row_gate[r] * y[r] is added at perm_token[r] (int32, from 0 to tokens - 1; perm_token and
+    row_gate have an element for each of a's rows, those of no group are not looked at)."""
     dev = _device()
+    if (perm_token is None) != (row_gate is None):
+        raise ValueError("perm_token and row_gate go together")
+    perm_token = _tensor(perm_token, "perm_token", _I32T, None, True, dev=dev, least=a.rows)
+    row_gate = _tensor(row_gate, "row_gate", _F32, None, True, dev=dev, least=a.rows)
     p = _tensor(out, "out", _FLOATS, (a.rows if perm_token is None else out.shape[0], a.K), dev=dev)
     _check(lib().moe_mx4_grouped_ffn(
         a.desc(dev), w_gate_up.desc(dev), w_down.desc(dev), _tensor(h_scale, "h_scale", _F32, (1,), True, dev=dev),
-        _tensor(perm_token, "perm_token", _I32T, None, True, dev=dev),
-        _tensor(row_gate, "row_gate", _F32, None, True, dev=dev), scale, p, _DTYPES[out.dtype],
+        perm_token, row_gate, scale, p, _DTYPES[out.dtype],
         _tensor(ws, "ws", _U8, dev=dev), ws.numel(), _stream(stream, dev)), "moe_mx4_grouped_ffn")
     return out
 

@@ -1,0 +1,50 @@
+"""What the 4-bit binding refuses before it calls the library (no GPU: the device is a stand-in)."""
+import ctypes
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from mixture_experts_layer_29_b200 import build, mx4
+
+
+@pytest.fixture
+def no_calls(monkeypatch):
+    """The current device is 0, and a call of the library fails the test."""
+    monkeypatch.setattr(mx4, "_device", lambda: 0)
+    monkeypatch.setattr(mx4, "_raw_stream", lambda dev: 0)
+
+    def called():
+        raise AssertionError("the library was called")
+
+    monkeypatch.setattr(mx4, "lib", called)
+
+
+def rows_of(n, K=256):
+    return SimpleNamespace(rows=n, K=K, groups=1, fmt="mxfp4", desc=lambda dev: None)
+
+
+@pytest.mark.parametrize("tok,gate,match", [
+    (torch.zeros(10, dtype=torch.int32), None, "go together"), (None, torch.zeros(10), "go together"),
+    (torch.zeros(9, dtype=torch.int32), torch.zeros(10), "perm_token: 9 elements, 10"),
+    (torch.zeros(10, dtype=torch.int32), torch.zeros(3, 3), "row_gate: 9 elements, 10"),
+    (torch.zeros(10, dtype=torch.int64), torch.zeros(10), "perm_token: torch.int64"),
+    (torch.zeros(10, dtype=torch.int32), torch.zeros(10, dtype=torch.bfloat16), "row_gate: torch.bfloat16")])
+def test_fused_combine_needs_a_token_and_a_gate_per_row(no_calls, monkeypatch, tok, gate, match):
+    if tok is not None and tok.numel() == 10 and tok.dtype == torch.int32 and gate is not None:
+        real = mx4._tensor          # let perm_token, which is right, pass though it is on the CPU
+        monkeypatch.setattr(mx4, "_tensor", lambda t, name, *a, **k: 0 if name == "perm_token" else real(t, name, *a, **k))
+    with pytest.raises(ValueError, match=match):
+        mx4.grouped_ffn(rows_of(10), rows_of(1024), rows_of(256), torch.zeros(4, 256), torch.zeros(8), None, tok, gate)
+
+
+def test_library_refuses_gates_without_tokens():
+    build.build()
+    L, good = mx4.lib(), 1 << 20
+    a = mx4.Desc(0, 256, 256, 2, 0, 0, good, None, good, good)
+    g = mx4.Desc(0, 1024, 256, 2, 512, 0, None, None, good, good)
+    d = mx4.Desc(0, 512, 256, 2, 256, 0, None, None, good, good)
+    n = ctypes.c_size_t(0)
+    assert L.moe_mx4_ffn_workspace_size(ctypes.byref(a), ctypes.byref(g), ctypes.byref(n)) == 0
+    args = (ctypes.byref(a), ctypes.byref(g), ctypes.byref(d), None)
+    assert L.moe_mx4_grouped_ffn(*args, None, good, 1.0, good, 1, good, n.value, None) == -1
