@@ -324,6 +324,7 @@ int moe_mx4_quantize(const moe_mx4_t* m, const void* x, int32_t dtype, int64_t l
   if (tokens == 0 || m->rows == 0) return MOE_OK;
   MOE_TRY(check_ptrs({x, m->codes, m->scales}));
   MOE_TRY(check_opt({row_of}));
+  if (reinterpret_cast<uintptr_t>(status) & 3u) return MOE_ERR_ALIGNMENT;
   QuantArgs q{};
   dim3 grid;
   int S;

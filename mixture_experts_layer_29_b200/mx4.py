@@ -174,6 +174,7 @@ def quantize_weight(w, fmt, tensor_scale=None, stream=None) -> Matrix:
 
 _FLOATS = (torch.bfloat16, torch.float32)
 _F32, _I32T, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
+_STATUS = (torch.uint8, torch.int32)
 
 
 def _tensors(dev, *args):
@@ -204,8 +205,8 @@ def _rows(t, name, K, rows, dev):
 def quantize(x, m: Matrix, row_of=None, status=None, stream=None) -> Matrix:
     """Rounds x into m. Without row_of, row r of m is row r of x [rows, K]. With row_of int32
     [tokens, picks] (abi.permute's), row t of x [tokens, K] goes to each row row_of[t, p] >= 0
-    of m. status: a device int32 that receives a device-side check's failure (a workspace's
-    first word, for abi.read_device_status)."""
+    of m. status: a device int32 that receives a device-side check's failure (or a workspace, in whose
+    first word abi.read_device_status looks for it)."""
     dev = _device()
     tokens, picks = m.rows, 0
     if row_of is not None:
@@ -215,7 +216,7 @@ def quantize(x, m: Matrix, row_of=None, status=None, stream=None) -> Matrix:
         row_of = _tensor(row_of, "row_of", _I32T, dev=dev)
     p, dt, ld = _rows(x, "x", m.K, tokens, dev)
     if status is not None:
-        status = _tensor(status, "status", (torch.uint8, torch.int32), dev=dev)
+        status = _tensor(status, "status", _STATUS, dev=dev, least=1 if getattr(status, "dtype", None) is torch.int32 else 4)
     _check(lib().moe_mx4_quantize(m.desc(dev), p, dt, ld, row_of, tokens, picks, status, _stream(stream, dev)),
            "moe_mx4_quantize")
     return m

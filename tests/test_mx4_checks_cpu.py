@@ -48,3 +48,21 @@ def test_library_refuses_gates_without_tokens():
     assert L.moe_mx4_ffn_workspace_size(ctypes.byref(a), ctypes.byref(g), ctypes.byref(n)) == 0
     args = (ctypes.byref(a), ctypes.byref(g), ctypes.byref(d), None)
     assert L.moe_mx4_grouped_ffn(*args, None, good, 1.0, good, 1, good, n.value, None) == -1
+
+
+@pytest.mark.parametrize("status,match", [
+    (torch.zeros(3, dtype=torch.uint8), "status: 3 elements, 4"), (torch.zeros(0, dtype=torch.int32), "status: 0 elements, 1"),
+    (torch.zeros(4, dtype=torch.int64), "status: torch.int64"), (torch.zeros(8, dtype=torch.uint8)[::2], "status: not contiguous"),
+    (7, "status: a tensor")])
+def test_quantize_needs_a_whole_status_word(no_calls, monkeypatch, status, match):
+    monkeypatch.setattr(mx4, "_rows", lambda *a: (0, 0, 256))
+    with pytest.raises(ValueError, match=match):
+        mx4.quantize(torch.zeros(10, 256), rows_of(10), None, status)
+
+
+def test_library_refuses_a_status_off_four_bytes():
+    build.build()
+    good = 1 << 20
+    m = mx4.Desc(0, 256, 256, 2, 128, 0, None, None, good, good)
+    call = mx4.lib().moe_mx4_quantize
+    assert [call(ctypes.byref(m), good, 0, 256, None, 256, 0, good + off, None) for off in (1, 2, 3)] == [-3, -3, -3]
