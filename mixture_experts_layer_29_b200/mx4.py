@@ -15,6 +15,7 @@ device and contiguity (ValueError). Inference only: the 4-bit product has no bac
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -78,6 +79,17 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 def _stream(stream, dev: int) -> int:
     return _raw_stream(dev) if stream is None else abi._stream(stream)
+
+
+@contextlib.contextmanager
+def _on(stream, dev: int):
+    """Makes `stream` (a stream, its handle, or None: the current one) the current stream, so that what a
+    call allocates and copies on the way is ordered with its kernels and belongs to their stream."""
+    if stream is None:
+        yield
+        return
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, dev) if isinstance(stream, int) else stream):
+        yield
 
 
 def _check(rc: int, where: str):
@@ -156,20 +168,25 @@ def allocate(fmt, rows, K, groups=1, offsets=None, tensor_scale=None, device="cu
 
 def from_checkpoint(fmt, codes, scales, tensor_scale=None, stream=None) -> Matrix:
     """A weight from a 4-bit checkpoint: codes [groups, N, K / 2] uint8 (used as they are) and
-    row-major block scales [groups, N, K / B] uint8, laid out for the tensor cores here, once."""
+    row-major block scales [groups, N, K / B] uint8, laid out for the tensor cores here, once.
+
+    Here and in quantize_weight, with a stream given, all of the work is queued on it, the matrix's memory
+    is that stream's, and the inputs have to be ready on it."""
     groups, N, half = codes.shape
-    m = Matrix(fmt, groups * N, 2 * half, groups, None, tensor_scale, codes=codes, device=codes.device)
-    p = _tensor(scales, "scales", (torch.uint8,), (groups, N, m.K // BLOCK[fmt]))
     dev = _device()
-    _check(lib().moe_mx4_pack_scales(m.desc(dev), p, _stream(stream, dev)), "moe_mx4_pack_scales")
+    with _on(stream, dev):
+        m = Matrix(fmt, groups * N, 2 * half, groups, None, tensor_scale, codes=codes, device=codes.device)
+        p = _tensor(scales, "scales", (torch.uint8,), (groups, N, m.K // BLOCK[fmt]))
+        _check(lib().moe_mx4_pack_scales(m.desc(dev), p, _raw_stream(dev)), "moe_mx4_pack_scales")
     return m
 
 
 def quantize_weight(w, fmt, tensor_scale=None, stream=None) -> Matrix:
-    """A weight [groups, N, K] bf16 or fp32 in 4 bits, once, at load time."""
+    """A weight [groups, N, K] bf16 or fp32, of any strides, in 4 bits, once, at load time."""
     groups, N, K = w.shape
-    m = Matrix(fmt, groups * N, K, groups, None, tensor_scale, device=w.device)
-    return quantize(w.reshape(groups * N, K), m, stream=stream)
+    with _on(stream, _device()):
+        m = Matrix(fmt, groups * N, K, groups, None, tensor_scale, device=w.device)
+        return quantize(w.reshape(groups * N, K), m)
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
