@@ -297,7 +297,7 @@ class Mx4MoELayer:
     are rounded once and written to its picks' rows.
 
     w_gate_up, w_down: Matrix (quantize_weight or from_checkpoint). x_scale, h_scale: the
-    activations' nvfp4 factors, fp32 [1], or None. forward(x) returns what
+    activations' nvfp4 factors, fp32 [1], or None. forward(x), x [T, H] bf16, returns what
     abi.MoELayer.forward returns."""
 
     def __init__(self, shape: abi.Shape, w_router, bias, w_gate_up: Matrix, w_down: Matrix,
@@ -309,6 +309,11 @@ class Mx4MoELayer:
                               ("w_down", w_down, (N, N * shape.H, shape.I))):
             if (m.groups, m.rows, m.K) != want or m.offsets is not None:
                 raise ValueError(f"{name}: {m.groups} groups of {m.rows} x {m.K} in all, expected {want}")
+        if w_down.fmt != w_gate_up.fmt:
+            raise ValueError(f"w_down: {w_down.fmt}, but w_gate_up is {w_gate_up.fmt}")
+        _tensor(w_router, "w_router", _F32, (shape.E, shape.H))
+        _tensor(bias, "bias", _F32, (shape.E,))
+        _tensor(h_scale, "h_scale", _F32, (1,), optional=True)
         self.shape, self.w_router, self.bias = shape, w_router, bias
         self.w_gate_up, self.w_down, self.h_scale, self.pid = w_gate_up, w_down, h_scale, pid
         dev = w_gate_up.codes.device
@@ -336,7 +341,9 @@ class Mx4MoELayer:
         abi.pid_init(shape, bias, self.pid_state)
 
     def forward(self, x, logits_in=None, stream=None):
-        s = self.shape
+        s, dev = self.shape, _device()
+        _tensor(x, "x", (torch.bfloat16,), (s.T, s.H), dev=dev)
+        _tensor(logits_in, "logits_in", _F32, (s.T, s.E), optional=True, dev=dev)
         abi.route(s, x, self.w_router, logits_in, self.bias, None if logits_in is not None else self.logits,
                   self.topk_idx, self.topk_gate, self.counts, self.nffn_hist, self.zgate, self.scratch, stream)
         abi.permute(s, self.topk_idx, self.topk_gate, self.zgate, x, self.offsets, self.perm_token,

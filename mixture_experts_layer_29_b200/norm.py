@@ -137,6 +137,8 @@ class MoEBlock:
         if normed is None:
             block_norm(self.before, residual, None, None, None, self.w_pre, None, self.x, stream=stream)
             normed = self.x
+        else:       # the layer's own call takes it as it is
+            _tensor(normed, "normed", (self.x.dtype,), self.x.shape)
         out = self.layer.forward(normed, stream=stream)[0][: self.layer.shape.T]
         return block_norm(self.after, residual, out, self.w_post, self.gate, w_next, self.residual_out,
                           None if w_next is None else self.normed, stream=stream)

@@ -5,7 +5,7 @@ from types import SimpleNamespace
 import pytest
 import torch
 
-from mixture_experts_layer_29_b200 import build, mx4
+from mixture_experts_layer_29_b200 import abi, build, mx4, norm
 
 
 @pytest.fixture
@@ -66,3 +66,50 @@ def test_library_refuses_a_status_off_four_bytes():
     m = mx4.Desc(0, 256, 256, 2, 128, 0, None, None, good, good)
     call = mx4.lib().moe_mx4_quantize
     assert [call(ctypes.byref(m), good, 0, 256, None, 256, 0, good + off, None) for off in (1, 2, 3)] == [-3, -3, -3]
+
+
+def layer(no_calls, monkeypatch):
+    monkeypatch.setattr(abi, "lib", lambda: pytest.fail("the library was called"))
+    lay = object.__new__(mx4.Mx4MoELayer)
+    lay.shape = abi.make_shape(8, 256, 128, 6, 2, 2, "bf16", "deterministic")
+    for name in ("w_router", "bias", "logits", "topk_idx", "topk_gate", "counts", "nffn_hist", "zgate", "scratch"):
+        setattr(lay, name, torch.zeros(8))
+    return lay
+
+
+@pytest.mark.parametrize("x,logits,match", [
+    (torch.zeros(7, 256, dtype=torch.bfloat16), None, "x: shape"), (torch.zeros(8, 256), None, "x: torch.float32"),
+    (torch.zeros(8, 512, dtype=torch.bfloat16)[:, :256], None, "x: not contiguous"),
+    (torch.zeros(8, 256, dtype=torch.bfloat16), None, "x: on cpu"), (None, None, "x: a tensor"),
+    ("right", torch.zeros(8, 7), "logits_in: shape"), ("right", torch.zeros(8, 8).double(), "logits_in: torch.float64")])
+def test_layer_looks_at_its_input_before_the_router_reads_it(no_calls, monkeypatch, x, logits, match):
+    lay, real = layer(no_calls, monkeypatch), mx4._tensor
+    if isinstance(x, str):
+        monkeypatch.setattr(mx4, "_tensor", lambda t, name, *a, **k: 0 if name == "x" else real(t, name, *a, **k))
+        x = torch.zeros(8, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match=match):
+        lay.forward(x, logits)
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(fmt="nvfp4"), "w_down: nvfp4"), (dict(router=torch.zeros(8, 255)), "w_router: shape"),
+    (dict(bias=torch.zeros(7)), "bias: shape"), (dict(h=torch.zeros(2)), "h_scale: shape")])
+def test_layer_looks_at_its_weights(no_calls, monkeypatch, kw, match):
+    real = mx4._tensor
+    monkeypatch.setattr(mx4, "_tensor", lambda t, name, *a, **k: 0 if t is None else real(t, name, *a, **k) if name in match else 0)
+    matrix = lambda n, rows, K, fmt: SimpleNamespace(groups=n, rows=rows, K=K, offsets=None, fmt=fmt)     # noqa: E731
+    with pytest.raises(ValueError, match=match):
+        mx4.Mx4MoELayer(abi.make_shape(8, 256, 128, 6, 2, 2, "bf16"), kw.get("router", torch.zeros(8, 256)),
+                        kw.get("bias", torch.zeros(8)), matrix(6, 6 * 256, 256, "mxfp4"),
+                        matrix(6, 6 * 256, 128, kw.get("fmt", "mxfp4")), h_scale=kw.get("h"))
+
+
+@pytest.mark.parametrize("normed,match", [(torch.zeros(7, 256, dtype=torch.bfloat16), "normed: shape"),
+                                          (torch.zeros(8, 256), "normed: torch.float32"),
+                                          (torch.zeros(256, 8, dtype=torch.bfloat16).T, "normed: not contiguous")])
+def test_block_looks_at_a_norm_that_it_is_given(no_calls, normed, match):
+    lay = SimpleNamespace(shape=abi.make_shape(8, 256, 128, 6, 2, 2, "bf16"), out=torch.zeros(8, 256, dtype=torch.bfloat16),
+                          forward=lambda *a, **k: pytest.fail("the layer was called"))
+    block = norm.MoEBlock(lay, torch.ones(256))
+    with pytest.raises(ValueError, match=match):
+        block.forward(torch.zeros(8, 256, dtype=torch.bfloat16), normed=normed)
