@@ -31,8 +31,8 @@ bool tune_value_ok(int knob, int64_t v) {
     case MOE_TUNE_PAIR_A_TRIM:
     case MOE_TUNE_PAIR_SWAP_AB:
     case MOE_TUNE_PAIR_STREAM_HINT:
-    case MOE_TUNE_PAIR_TAILS:
-    case MOE_TUNE_TEST_STALL: return v == 0 || v == 1;
+    case MOE_TUNE_PAIR_TAILS: return v == 0 || v == 1;
+    case MOE_TUNE_TEST_STALL: return v >= 0 && v <= 2;
     case MOE_TUNE_GEMM_PAIR: return v >= -1 && v <= 1;
     case MOE_TUNE_ROUTER_N: return v == 0 || v == 192 || v == 256;
     case MOE_TUNE_ROUTER_MIN_SPLIT: return v >= 1 && v <= 1024;
@@ -50,7 +50,10 @@ bool tune_value_ok(int knob, int64_t v) {
 
 int64_t tuning(int knob) { return g_tune[knob].load(std::memory_order_relaxed); }
 
-bool take_test_stall() { return g_tune[MOE_TUNE_TEST_STALL].exchange(0) != 0; }
+bool take_test_stall(int which) {
+  int64_t v = which;
+  return g_tune[MOE_TUNE_TEST_STALL].compare_exchange_strong(v, 0);
+}
 
 bool pdl_enabled() { return tuning(MOE_TUNE_PDL) != 0; }
 

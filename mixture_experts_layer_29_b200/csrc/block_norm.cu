@@ -378,14 +378,15 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd(const BwdArgs a) {
 // Rows through a ring in shared memory, filled by bulk copies: a CTA of a wide row has an SM to itself
 // (its sums over tokens stay in registers), so the loads of the next tokens go on under the two block
 // reductions of this one. (Loading the next token into registers instead gained nothing: 169 us for
-// 8192 x 6144 bf16.) The ring has `depth` tokens of up to four rows. A CTA of at most 512 threads may use
+// 8192 x 6144 bf16.) The ring has `depth` tokens of up to four rows (stall: testing, MOE_TUNE_TEST_STALL, the
+// first place of CTA 0 is not filled). A CTA of at most 512 threads may use
 // 128 registers a thread: with the parameters and both vectors' sums in them 4096 x 8192 bf16 take 86 us
 // instead of 148 with the parameters read for every token, 4096 x 6144 fp32 119 instead of 137.
 constexpr int kMaxDepth = 4;
 constexpr int kRingThreads = 768;      // what the register file holds with their sums
 
 template <typename T, int VPT, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_block_norm_bwd_ring(const BwdArgs a, int depth) {
+__global__ void __launch_bounds__(THREADS) k_block_norm_bwd_ring(const BwdArgs a, int depth, int stall) {
   constexpr int N = Row<T>::N;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float part[2][32];
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(THREADS) k_block_norm_bwd_ring(const BwdArgs a
         bulk_load(ring + (size_t)(s * 4 + i) * row, static_cast<const char*>(src[i]) + t * row, row, &full[s]);
   };
   if (threadIdx.x == 0)
-    for (int s = 0; s < depth; ++s)
+    for (int s = blockIdx.x ? 0 : stall; s < depth; ++s)
       if (blockIdx.x + (size_t)s * gridDim.x < (size_t)a.T) fill(s, blockIdx.x + (size_t)s * gridDim.x);
 
   // the columns' parameters stay in registers
@@ -426,11 +427,12 @@ __global__ void __launch_bounds__(THREADS) k_block_norm_bwd_ring(const BwdArgs a
   const float inv_h = 1.0f / (float)a.H;
   int s = 0;
   uint32_t phase = 0;
+  bool ok = true;
   for (size_t t = blockIdx.x; t < (size_t)a.T; t += gridDim.x) {
     const TokenScalars k = load_scalars(a, t);
-    // (after a wait that ran out the thread works on what there is: it has to keep up with the
-    // block's barriers)
-    mbar_wait(&full[s], phase, &abort_flag);
+    // (a thread whose wait ran out works on what there is, since it has to keep up with the block's
+    // barriers, and waits for no token after that)
+    ok = ok && mbar_wait(&full[s], phase, &abort_flag);
     uint4 qd[VPT], qb[VPT];
     float g[VPT][N], rhat[VPT][N];
     const auto vec = [&](bool have, int i, int v) {
@@ -466,7 +468,12 @@ __global__ void __launch_bounds__(THREADS) k_block_norm_bwd_ring(const BwdArgs a
   }
   store_partial<T, VPT>(a, nvec, s_post, s_pre);
   __syncthreads();
-  if (abort_flag && threadIdx.x == 0) set_status(a.status, MOE_ERR_TIMEOUT);
+  if (abort_flag && threadIdx.x == 0) {
+    set_status(a.status, MOE_ERR_TIMEOUT);
+    // let copies already in flight land before the CTA's memory goes away
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+  }
 }
 
 // Sums the CTAs' partial sums p (blockIdx.y 0: d_w_post = scale * gate_c * p and d_gate_c = scale *
@@ -651,7 +658,7 @@ int moe_block_norm_backward(const moe_norm_t* n, const void* d_residual_out, con
       // between this call's setting and its launch
       if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes) != cudaSuccess)
         return MOE_ERR_CUDA;
-      e = launch_kernel(kern, grid, b.threads, b.smem, st, 1, a, b.depth);
+      e = launch_kernel(kern, grid, b.threads, b.smem, st, 1, a, b.depth, take_test_stall(2) ? 1 : 0);
     } else {
       // more than 12288 (bf16) or 6144 (fp32) elements: 2, or 2 to 4 vectors
       auto kern = bf16         ? k_block_norm_bwd<__nv_bfloat16, 2>

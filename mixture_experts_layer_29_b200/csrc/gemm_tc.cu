@@ -1633,7 +1633,7 @@ int launch_grouped_ffn_tc(const void* x, const void* x_perm, const int32_t* offs
   g1.kb_per_split = g1.kblocks;
   g1.half_tiles = pair ? pair_half_tiles() : 0;
   g1.band = band_of(MOE_TUNE_GATE_UP_BAND);
-  g1.test_stall = take_test_stall() ? 1 : 0;
+  g1.test_stall = take_test_stall(1) ? 1 : 0;
   // CTA pairs: an expert's whole 256-row tiles on the pair kernel, the rest of its rows
   // (at most 128) on the one-CTA kernel (pair_rows), each GEMM as two launches
   const bool split = pair && tuning(MOE_TUNE_PAIR_TAILS) != 0;

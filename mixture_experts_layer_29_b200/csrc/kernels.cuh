@@ -23,8 +23,8 @@ void count_launch(int n = 1);
 
 // Current value of a moe_set_tuning switch (MOE_TUNE_*).
 int64_t tuning(int knob);
-// Reads and clears MOE_TUNE_TEST_STALL: true once per arming.
-bool take_test_stall();
+// Clears MOE_TUNE_TEST_STALL if it has this value: true once per arming.
+bool take_test_stall(int which);
 
 struct DeviceInfo {
   int device = -1;
