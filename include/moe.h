@@ -138,7 +138,8 @@ uint64_t moe_launch_count(void);
  *                             the status word; that call's outputs are undefined. The
  *                             switch returns to 0 when that launch is queued. Set to 2, the
  *                             same for the first token of the next moe_block_norm_backward
- *                             whose rows go through shared memory (moe_norm.h).
+ *                             whose rows go through shared memory (moe_norm.h); to 3, for the
+ *                             first stage of the first tile of the next 4-bit product (moe_mx4.h).
  *   MOE_TUNE_GATE_UP_BAND     0 (default): the library's choice; 1 to 64: the CTA-pair
  *   MOE_TUNE_DOWN_BAND        gate/up (down) GEMM visits an expert's 256-row M tiles in
  *                             bands of this many, each band N tile by N tile with its M

@@ -32,7 +32,7 @@ bool tune_value_ok(int knob, int64_t v) {
     case MOE_TUNE_PAIR_SWAP_AB:
     case MOE_TUNE_PAIR_STREAM_HINT:
     case MOE_TUNE_PAIR_TAILS: return v == 0 || v == 1;
-    case MOE_TUNE_TEST_STALL: return v >= 0 && v <= 2;
+    case MOE_TUNE_TEST_STALL: return v >= 0 && v <= 3;
     case MOE_TUNE_GEMM_PAIR: return v >= -1 && v <= 1;
     case MOE_TUNE_ROUTER_N: return v == 0 || v == 192 || v == 256;
     case MOE_TUNE_ROUTER_MIN_SPLIT: return v >= 1 && v <= 1024;

@@ -106,6 +106,7 @@ struct Args {
   const float* row_gate;
   float scale;
   int* status;
+  int test_stall;         // testing (MOE_TUNE_TEST_STALL): tile 0 leaves its first stage unloaded
 };
 
 // CPS: scale pieces of a stage along K (2: MXFP4, 4: NVFP4); NT: rows of a tile
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kb = 0; kb < g.kstages; ++kb) {
         ok = warp_wait(&s.empty[stage], phase ^ 1u, abort_flag);
         if (!ok) break;
-        if (elect_one()) {
+        if (!(g.test_stall && tile + kb == 0) && elect_one()) {
           uint8_t* st = s.ring[stage];
           uint64_t* bar = &s.full[stage];
           const uint32_t sfb = 512u * (uint32_t)min(CPS, g.chunks - kb * CPS);
@@ -902,7 +903,7 @@ __global__ void __launch_bounds__(pair_threads(MODE), 1)
         if (!ok) break;
         const int next = stage + 1 == STAGES ? 0 : stage + 1;
         ready = mbar_test(&s.empty[next], next ? phase ^ 1u : phase);
-        if (elect_one()) {
+        if (!(g.test_stall && tile + kb == 0) && elect_one()) {      // (neither CTA loads)
           uint8_t* st = s.ring[stage];
           const uint32_t full = mapa_shared(smem_u32(&s.full[stage]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * (W_BYTES + mine * 128));
@@ -1263,6 +1264,7 @@ int launch_product(const moe_mx4_t& a, const moe_mx4_t& w, Args g, const DeviceI
   g.a_factor = a.factor;
   g.w_factor = w.factor;
   g.w_factor_per_group = w.factor_per_group;
+  g.test_stall = take_test_stall(3) ? 1 : 0;
   // Up to 64 rows per group on average (of the rows there may be): one CTA per tile.
   const bool few = a.rows <= 64ll * a.groups;
 #define MX4_LAUNCH(KERNEL, CPS)                                              \

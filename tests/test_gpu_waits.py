@@ -6,10 +6,10 @@ import time
 import pytest
 import torch
 
-from mixture_experts_layer_29_b200 import abi, norm
+from mixture_experts_layer_29_b200 import abi, mx4, norm
 
 pytestmark = pytest.mark.gpu
-NORM = 2
+NORM, PRODUCT = 2, 3
 
 
 def stalled(which, call):
@@ -50,3 +50,31 @@ def test_norm_gradients_wait_that_runs_out(cuda_device, T, H, parts):
     call()
     assert abi.read_device_status(ws) == 0
     assert all(o is None or torch.equal(o, v) for o, v in zip(outs, want))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("rows", [90, 900])                     # one CTA per tile, and CTA pairs
+@pytest.mark.parametrize("what", ["bf16", "fp32", "ffn"])
+def test_product_wait_that_runs_out(cuda_device, fmt, rows, what):
+    """Two groups, many tiles; thirteen stages along K, more than either ring has."""
+    groups, K, I = 2, 3200, 1024
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn(rows, K, device="cuda", generator=g).to(torch.bfloat16)
+    off = torch.tensor([0, rows // 3, rows], dtype=torch.int32, device="cuda")
+    a = mx4.quantize(x, mx4.allocate(fmt, rows, K, groups, off))
+    w = mx4.quantize_weight(torch.randn(groups, 2 * I, K, device="cuda", generator=g) * 0.02, fmt)
+    d = mx4.quantize_weight(torch.randn(groups, K, I, device="cuda", generator=g) * 0.02, fmt)
+    if what == "ffn":
+        out, ws = torch.empty(rows, K, device="cuda"), mx4.ffn_workspace(a, w)
+        call = lambda: mx4.grouped_ffn(a, w, d, out, ws)                                        # noqa: E731
+    else:
+        out = torch.empty(rows, 2 * I, device="cuda", dtype=torch.bfloat16 if what == "bf16" else torch.float32)
+        ws = mx4.gemm_workspace()
+        call = lambda: mx4.grouped_gemm(a, w, out, ws)                                          # noqa: E731
+    call()
+    assert abi.read_device_status(ws) == 0
+    want = out.clone()
+    took = stalled(PRODUCT, call)
+    assert abi.read_device_status(ws) == -7 and 1.5 < took < 8, took
+    call()
+    assert abi.read_device_status(ws) == 0 and torch.equal(out, want)
