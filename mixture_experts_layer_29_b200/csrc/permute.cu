@@ -359,8 +359,11 @@ cudaError_t launch_permute(const int32_t* topk_idx, const float* topk_gate, cons
     // one CTA for the indices, then a wide copy (short chain for small batches)
     const size_t smem = sizeof(uint32_t) * (size_t)n_ffn * ((T + 31) / 32) * 2 + sizeof(int32_t) * (n_ffn + 1);
     if (smem > 48 * 1024) {
+      // the largest batch's and layer's, whatever this call's: another thread's call may set the kernel's limit
+      // between this one's setting and its launch
+      const size_t most = sizeof(uint32_t) * 1024 * ((kSmallT + 31) / 32) * 2 + sizeof(int32_t) * 1025;
       const cudaError_t e = cudaFuncSetAttribute(k_perm_index_small,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
       if (e != cudaSuccess) return e;
     }
     cudaError_t e = launch_kernel(k_perm_index_small, 1, 512, smem, st, 1, topk_idx, topk_gate, T,

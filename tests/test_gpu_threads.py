@@ -5,7 +5,7 @@ import threading
 import pytest
 import torch
 
-from mixture_experts_layer_29_b200 import norm
+from mixture_experts_layer_29_b200 import abi, norm
 
 pytestmark = pytest.mark.gpu
 
@@ -42,6 +42,41 @@ def test_norm_gradients_of_two_shapes_from_several_threads(cuda_device):
                 errors.append((H, codes))
 
     threads = [threading.Thread(target=work, args=(H,)) for H in widths]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
+def test_permutations_of_two_layers_from_several_threads(cuda_device):
+    """Layers of different numbers of experts share the small batches' kernel, not its shared memory."""
+    T, n_ffn, K, H, calls = 512, (1000, 400), 4, 128, 3000
+    L, errors, start = abi.lib(), [], threading.Barrier(6)
+
+    def work(n):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            b = abi.StepBuffers.allocate(abi.make_shape(T, H, 128, n, 0, K, "bf16", "deterministic"))
+            g = torch.Generator(device="cuda").manual_seed(n)
+            idx = torch.rand(T, n, device="cuda", generator=g).argsort(1)[:, :K].int().contiguous()
+            gate = torch.ones(T, K, device="cuda")
+            b.zgate.zero_()
+            x = torch.randn(T, H, device="cuda", generator=g).bfloat16()
+            args = (b.shape, idx, gate, b.zgate, x, b.offsets, b.perm_token, b.row_of, b.row_gate, b.x_perm, None, b.ws)
+            abi.permute(*args)
+            want = b.row_of.clone()
+            b.row_of.fill_(-9)
+            p = [None if t is None else t.data_ptr() for t in args[1:]]
+            shape, ws = ctypes.byref(b.shape), b.ws.numel()
+            st.synchronize()
+            start.wait()
+            codes = {L.moe_permute(shape, *p, ws, st.cuda_stream) for _ in range(calls)}
+            st.synchronize()
+            if codes != {0} or not torch.equal(b.row_of, want):
+                errors.append((n, codes))
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in n_ffn * 3]
     for t in threads:
         t.start()
     for t in threads:
