@@ -136,11 +136,11 @@ class Matrix:
         n = _SZ(0)
         _check(lib().moe_mx4_scale_bytes(ctypes.byref(d), ctypes.byref(n)), "moe_mx4_scale_bytes")
         codes = torch.empty(rows, K // 2, dtype=torch.uint8, device=device) if codes is None else codes
+        d.codes = _tensor(codes, "codes", (torch.uint8,), least=rows * (K // 2))
         scales = torch.empty(n.value, dtype=torch.uint8, device=device)
         self._parts = (fmt, rows, K, groups, offsets, tensor_scale, codes.view(rows, K // 2), scales)
         d.offsets = _tensor(offsets, "offsets", (torch.int32,), (groups + 1,), optional=True)
         d.factor = _tensor(tensor_scale, "tensor_scale", (torch.float32,), optional=True)
-        d.codes = _tensor(codes, "codes", (torch.uint8,))
         d.scales = _tensor(scales, "scales", (torch.uint8,))
         self._dev = codes.get_device()
 

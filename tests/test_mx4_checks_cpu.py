@@ -113,3 +113,20 @@ def test_block_looks_at_a_norm_that_it_is_given(no_calls, normed, match):
     block = norm.MoEBlock(lay, torch.ones(256))
     with pytest.raises(ValueError, match=match):
         block.forward(torch.zeros(8, 256, dtype=torch.bfloat16), normed=normed)
+
+
+@pytest.mark.parametrize("codes,match", [(torch.zeros(2, 8, 256, dtype=torch.uint8)[:, :, ::2], "codes: not contiguous"),
+                                         (torch.zeros(2, 8, 128), "codes: torch.float32"),
+                                         (torch.zeros(2, 8, 128, dtype=torch.uint8), "codes: on cpu")])
+def test_checkpoint_codes_are_looked_at_first(monkeypatch, codes, match):
+    build.build()
+    monkeypatch.setattr(mx4, "_device", lambda: 0)
+    with pytest.raises(ValueError, match=match):
+        mx4.from_checkpoint("mxfp4", codes, torch.zeros(2, 8, 8, dtype=torch.uint8))
+
+
+def test_matrix_needs_all_of_its_codes(monkeypatch):
+    build.build()
+    monkeypatch.setattr(mx4, "_device", lambda: 0)
+    with pytest.raises(ValueError, match="codes: 384 elements, 512"):
+        mx4.Matrix("mxfp4", 4, 256, codes=torch.zeros(3, 128, dtype=torch.uint8), device="cpu")
