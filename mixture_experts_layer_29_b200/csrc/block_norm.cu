@@ -11,8 +11,8 @@
 //   d_gate = s sum g n1,  d_w_post = sum_t dn1 bhat,  d_w_pre = sum_t d_n2 rhat
 //
 // Bound by memory: 4 rows of H elements in and out per token forward, 6 backward, against some
-// 10 and 22 flops per element (the backward's done two at a time: 119 us instead of 123 for 8192 x 6144
-// bf16, 151 instead of 186 for 4096 x 8192). One CTA holds a token's row in registers (16-byte vectors), so
+// 10 and 22 flops per element (the backward's done two at a time, which took 3 % off 8192 x 6144 bf16 and a
+// fifth off 4096 x 8192): 70 and 112 us for 8192 x 6144 bf16, 5.8 and 5.4 TB/s. One CTA holds a token's row in registers (16-byte vectors), so
 // each array is read once; the two norms are two block reductions in a row, the second on what
 // the first produced. Forward: one CTA per token. Backward: persistent CTAs, so that the sums
 // over tokens (d_w_post, d_w_pre, d_gate per channel) stay in registers; each CTA writes its
@@ -200,8 +200,8 @@ struct BwdArgs {
   int* status;
 };
 
-// A token's norms and gate. (Loading them a token ahead is slower: 155 us instead of 132 for
-// 8192 x 6144 bf16.)
+// A token's norms and gate. (Loading them a token ahead was a sixth slower for 8192 x 6144
+// bf16.)
 struct TokenScalars {
   float rr, rb, gt;
 };
@@ -377,11 +377,12 @@ __global__ void __launch_bounds__(1024) k_block_norm_bwd(const BwdArgs a) {
 
 // Rows through a ring in shared memory, filled by bulk copies: a CTA of a wide row has an SM to itself
 // (its sums over tokens stay in registers), so the loads of the next tokens go on under the two block
-// reductions of this one. (Loading the next token into registers instead gained nothing: 169 us for
-// 8192 x 6144 bf16.) The ring has `depth` tokens of up to four rows (stall: testing, MOE_TUNE_TEST_STALL, the
-// first place of CTA 0 is not filled). A CTA of at most 512 threads may use
-// 128 registers a thread: with the parameters and both vectors' sums in them 4096 x 8192 bf16 take 86 us
-// instead of 148 with the parameters read for every token, 4096 x 6144 fp32 119 instead of 137.
+// reductions of this one. (Loading the next token into registers instead gained nothing.) The ring has
+// `depth` tokens of up to four rows (stall: testing, MOE_TUNE_TEST_STALL, the first place of CTA 0 is not
+// filled). A CTA of at most 512 threads may use 128 registers a thread: with the parameters and both vectors'
+// sums in them 4096 x 8192 bf16 take 84 us instead of 148 with the parameters read for every token, 4096 x
+// 6144 fp32 119 instead of 137. (bf16 rows of 8208 to 12288 columns, 1026 to 1536 vectors, have 80 registers
+// and spill some 90 of them: 200 us for 4096 x 12288, 45 % of the copy rate.)
 constexpr int kMaxDepth = 4;
 constexpr int kRingThreads = 768;      // what the register file holds with their sums
 
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(THREADS) k_block_norm_bwd_ring(const BwdArgs a
         });
     // every thread has used its rows before the token's last barrier (loads that are only under way
     // there would not do): the place is free. Filling it at the end of the token keeps the copies'
-    // issue, some 140 cycles each, out of the block's way (17 us of 132 for 8192 x 6144 bf16)
+    // issue, some 140 cycles each, out of the block's way (an eighth of the time for 8192 x 6144 bf16)
     const size_t next = t + (size_t)depth * gridDim.x;
     if (threadIdx.x == 0 && next < (size_t)a.T) fill(s, next);
     if (++s == depth) {
@@ -546,10 +547,11 @@ BwdShape bwd_shape(const moe_norm_t& n) {
   const bool narrow = nvec <= 2 * kRingThreads;
   row_shape(nvec, narrow ? kRingThreads : 1024, &b.vpt, &b.threads);
   b.per_sm = max(1, kRingThreads / b.threads);
-  // With one vector per thread CTAs of a third to a half of those threads leave the rest unused; CTAs of
-  // two vectors (128 registers a thread in bf16) then hold at least twice as much of the rows: 8192 x 4096
-  // bf16 75 us instead of 94, x 2048 fp32 77 instead of 83. (Where one vector fills the SM two cost: 131 us
-  // instead of 117 at 6144; and so they do with few tokens per CTA: 13.1 instead of 11.2 for 512 x 2048.)
+  // One-vector CTAs that make up at most three quarters of those 768 threads (a row of 288, or of 416 to 576
+  // threads) leave the rest unused. CTAs of two vectors take their place where together they have as many
+  // threads (768 in fp32; in bf16, with 128 registers a thread, 512, which rows of 416 to 512 threads meet):
+  // 8192 x 4096 bf16 75 us instead of 94, x 2048 fp32 77 instead of 83. (Where one vector fills the SM two
+  // cost: an eighth more at 6144; and so they do with few tokens per CTA: 13.1 instead of 11.2 for 512 x 2048.)
   if (b.vpt == 1 && n.T >= 2048 && 4 * b.per_sm * b.threads <= 3 * kRingThreads) {
     int vpt, threads;
     row_shape(nvec, (nvec + 1) / 2, &vpt, &threads);

@@ -80,7 +80,7 @@ constexpr int W_BYTES = 128 * 128;                  // a weight block's stage: 1
 enum Mode : int { kStore = 0, kFp32 = 1, kSwiglu = 2 };
 
 // Pair kernel: plain products have a third epilogue warp per quarter (17081 rows of the 768-wide layer
-// in 20.2 us instead of 21.5). The rounding of h gains nothing by one, and it takes issue slots from the
+// in 20.2 us instead of 21.5, 20.6 now). The rounding of h gains nothing by one, and it takes issue slots from the
 // other roles (229 to 236 us instead of 221 for 16384 rows' gate and up).
 constexpr int pair_epi_warps(int mode) { return mode == kSwiglu ? kEpiWarps : 12; }
 constexpr int pair_threads(int mode) { return (2 + pair_epi_warps(mode) + 2 * kScaleWarps + 1) * 32; }
@@ -408,8 +408,8 @@ __device__ __forceinline__ void prescale(uint32_t (&v)[N], float by) {
 // where the last places decide which way a value goes that lies half way between two numbers. (With __expf
 // and __fdividef up to 16 of the 33 million elements of 16384 rows' h went another way than by fp32's own
 // operations, with these none does.) The reciprocal is the hardware's estimate with one step of Newton's
-// method on 1 / d; d infinite (x below -88) gives 0. 384 us for 16384 rows' FFN; by expf and a division 388,
-// by the fast forms 378.
+// method on 1 / d; d infinite (x below -88) gives 0. It costs 16384 rows' FFN 2 % (373 us), expf and a
+// division 3 %.
 __device__ __forceinline__ float swiglu(float x, float u) {
   const float d = 1.0f + expf(-x);
   float r;
@@ -1030,7 +1030,7 @@ __global__ void __launch_bounds__(pair_threads(MODE), 1)
         if ((turn ^ 1) != set) continue;
         ok = warp_wait(&s.sland[stage], phase, abort_flag);
         if (!ok) break;
-        // pieces past the row's end hold an earlier stage's scales: written, never used
+        // (pieces past the row's end are zeros: written, never used)
         const uint8_t* sf = s.sring[stage] + lane * 16;
         uint4 w[CPS], r[CPS];
         uint2 r2[CPS];
@@ -1265,7 +1265,15 @@ int launch_product(const moe_mx4_t& a, const moe_mx4_t& w, Args g, const DeviceI
   g.w_factor = w.factor;
   g.w_factor_per_group = w.factor_per_group;
   g.test_stall = take_test_stall(3) ? 1 : 0;
-  // Up to 64 rows per group on average (of the rows there may be): one CTA per tile.
+  // Up to 64 rows per group on average (of the rows there may be: the host does not know the groups' sizes):
+  // one CTA per tile. In us, one CTA / pairs, MXFP4, 512 groups with 4096 x 6144 weights, of which some have
+  // rows, as many each:
+  //   rows each        16          64          96          128         256        512
+  //   512 groups   1024 / 1132 1104 / 1235 2147 / 1320 1959 / 1413
+  //   60            130 / 135   140 / 143   178 / 149   188 / 156   337 / 256   697 / 402
+  //   20             56 / 57     61 / 60     73 / 62     75 / 63    122 / 90    235 / 137
+  // The border is 64 rows of a group that has any. Where few of many groups have them, the rule keeps to the
+  // one-CTA kernel past it.
   const bool few = a.rows <= 64ll * a.groups;
 #define MX4_LAUNCH(KERNEL, CPS)                                              \
   (swiglu             ? KERNEL<CPS, kSwiglu>(a, w, g, dev, st)               \

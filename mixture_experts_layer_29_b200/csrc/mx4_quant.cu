@@ -6,9 +6,9 @@
 //  * quantise: a lane holds 16 elements (32 bytes of bf16 in one load, 8 bytes of codes), which are an
 //    NVFP4 block, or half of an MXFP4 one whose largest magnitude takes one shuffle; the four scale
 //    bytes of a piece's row go out as one word. With 8 elements per lane twice as many lanes worked out
-//    each scale: 8192 rows of 6144 to NVFP4 took 35.6 us instead of 26.1 (4.9 TB/s), 32768 to MXFP4 89
+//    each scale: 8192 rows of 6144 to NVFP4 took 35.6 us instead of 26.6 (4.8 TB/s), 32768 to MXFP4 89
 //    instead of 76 (6.6 TB/s, the card's copy rate). A warp takes up to 3 steps of 512 elements of a row
-//    (4 steps: 74.8 and 26.3 us, and 2.24 instead of 2.05 for 128 rows), all their loads in flight at
+//    (4 steps: 2 % less for the latter, nothing for the former, and 2.24 us instead of 2.05 for 128 rows), all their loads in flight at
 //    once, and looks for the row's group once for them.
 //  * dequantise: 8 elements per lane, up to 6 steps of 256 elements per warp (23 us for 8192 rows of
 //    6144 from NVFP4; 33.5 with the values made by integer operations instead of conversions).
