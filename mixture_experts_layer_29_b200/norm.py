@@ -120,7 +120,11 @@ class MoEBlock:
     None; gate fp32 [T] or [H] with its kind, or None. forward(residual, w_next) returns
     (residual_out, normed): the stream after the block and, with w_next [H], its norm before
     the next block (None without). Called with `normed` of a previous block, the norm before
-    this one is that block's and is not computed again."""
+    this one is that block's and is not computed again. Both are the block's own buffers, which its
+    next forward writes again.
+
+    Forward only: it keeps no rstd. Training calls block_norm with the rstd_* outputs and
+    block_norm_backward around abi.run_steps and abi.backward."""
 
     def __init__(self, layer, w_pre, w_post=None, gate=None, gate_kind="none", eps=1e-5, scale=1.0):
         s = layer.shape
