@@ -88,7 +88,9 @@ def _on(stream, dev: int):
     if stream is None:
         yield
         return
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, dev) if isinstance(stream, int) else stream):
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(abi._stream(stream), dev)
+    with torch.cuda.stream(stream):
         yield
 
 

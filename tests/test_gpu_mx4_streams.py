@@ -1,4 +1,6 @@
 """Weights made on a stream of their own while the current stream is busy."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -44,3 +46,15 @@ def test_weights_on_another_stream_do_not_wait_for_the_current_one(cuda_device, 
                 torch.equal(b.scales[at], byte.flatten(0, 1))]
     torch.cuda.synchronize()
     assert all(same) and junk
+
+
+@pytest.mark.parametrize("kind", ["default handle", "object"])
+def test_weights_on_streams_that_are_not_torchs(cuda_device, kind):
+    """The legacy default stream by its handle, and any object that has a handle."""
+    w = torch.randn(2, 128, 256, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    want = mx4.quantize_weight(w, "mxfp4")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = mx4.quantize_weight(w, "mxfp4", stream=0 if kind == "default handle" else SimpleNamespace(cuda_stream=st.cuda_stream))
+    torch.cuda.synchronize()
+    assert torch.equal(got.codes, want.codes)
