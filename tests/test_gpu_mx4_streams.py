@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 
 
 def busy():
-    torch.cuda._sleep(400_000_000)          # some 0.2 s on the current stream
+    torch.cuda._sleep(1_000_000_000)        # some half a second on the current stream
 
 
 @pytest.mark.parametrize("handle", [False, True])
